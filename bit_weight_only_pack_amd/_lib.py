@@ -76,6 +76,8 @@ SIGNATURES = {
     "lowbit_gemv_w4a8_batched_workspace_bytes": (_sz, [_i, _i, _i, _i, _vp]),
     "lowbit_gemv_w4a8_batched": (_i, [_i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "lowbit_gemv_w4a8_batched_noalloc": (_i, [_i, _i, _i, _i, _vp, _vp]),
+    "lowbit_gemm_w8a8": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
+    "lowbit_gemm_w8a8_workspace_bytes": (_sz, [_i, _i, _i]),
     "lowbit_gemv_chain_bytes": (_sz, [_i, _i]),
     "lowbit_gemv_chain_init": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, ctypes.c_uint, _vp, _sz, _vp]),
     "lowbit_gemv_chain_run": (_i, [_vp, _vp]),
@@ -90,6 +92,12 @@ SIGNATURES = {
     "lowbit_moe_combine": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "lowbit_moe_layer_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "lowbit_moe_layer": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]),
+    "lowbit_moe_sort": (_i, [_vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "lowbit_moe_sort_workspace_bytes": (_sz, [_i, _i, _i]),
+    "lowbit_moe_permute": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "lowbit_moe_unpermute": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "lowbit_moe_unpermute_backward": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "lowbit_moe_gemm_w8a8": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp]),
 }
 
 
@@ -297,3 +305,44 @@ def lowbit_gemv_chain_error(chain, stream=None):
     v = ctypes.c_uint(0)
     st = lib().lowbit_gemv_chain_error(ctypes.byref(chain), ctypes.byref(v), _stream(stream))
     return st, v.value
+
+
+def lowbit_gemm_w8a8(M, N, K, xq, x_scale, wq, w_scale, bias, y, y_dtype, workspace=None, ws_bytes=0, stream=None):
+    return lib().lowbit_gemm_w8a8(M, N, K, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias), _ptr(y),
+                                  y_dtype, _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def lowbit_gemm_w8a8_workspace_bytes(M, N, K):
+    return lib().lowbit_gemm_w8a8_workspace_bytes(M, N, K)
+
+
+def lowbit_moe_sort(topk_ids, T, top_k, E, expert_map, E_local, row_slot, slot_row, expert_offsets, workspace=None,
+                    ws_bytes=0, stream=None):
+    return lib().lowbit_moe_sort(_ptr(topk_ids), T, top_k, E, _ptr(expert_map), E_local, _ptr(row_slot),
+                                 _ptr(slot_row), _ptr(expert_offsets), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def lowbit_moe_sort_workspace_bytes(T, top_k, E_local):
+    return lib().lowbit_moe_sort_workspace_bytes(T, top_k, E_local)
+
+
+def lowbit_moe_permute(x, x_scale, T, top_k, row_bytes, slot_row, xp, xp_scale, stream=None):
+    return lib().lowbit_moe_permute(_ptr(x), _ptr(x_scale), T, top_k, row_bytes, _ptr(slot_row), _ptr(xp),
+                                    _ptr(xp_scale), _stream(stream))
+
+
+def lowbit_moe_unpermute(yp, dtype, weights, T, top_k, H, slot_row, y, stream=None):
+    return lib().lowbit_moe_unpermute(_ptr(yp), dtype, _ptr(weights), T, top_k, H, _ptr(slot_row), _ptr(y),
+                                      _stream(stream))
+
+
+def lowbit_moe_unpermute_backward(dy, yp, dtype, weights, T, top_k, H, slot_row, dyp, dweights, stream=None):
+    return lib().lowbit_moe_unpermute_backward(_ptr(dy), _ptr(yp), dtype, _ptr(weights), T, top_k, H, _ptr(slot_row),
+                                               _ptr(dyp), _ptr(dweights), _stream(stream))
+
+
+def lowbit_moe_gemm_w8a8(E, N, K, wq, w_scale, xq, x_scale, x_rows, row_slot, row_div, expert_offsets, rows, y,
+                         y_dtype, stream=None):
+    return lib().lowbit_moe_gemm_w8a8(E, N, K, _ptr(wq), _ptr(w_scale), _ptr(xq), _ptr(x_scale), x_rows,
+                                      _ptr(row_slot), row_div, _ptr(expert_offsets), rows, _ptr(y), y_dtype,
+                                      _stream(stream))

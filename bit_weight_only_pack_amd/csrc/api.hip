@@ -708,4 +708,149 @@ int lowbit_moe_layer(const void *w13, const void *w2, int E_local, int E, int H,
     return hip_status(e);
 }
 
+namespace {
+// Sizes the W8A8 and sorting kernels take: their grids have one workgroup per
+// token or 16 channels at least, and a grid holds fewer than 2^32 threads.
+constexpr int64_t kGridLimit = (int64_t)1 << 24;
+// int8 x int8 sums fit int32: 2^14 * K < 2^31
+constexpr int kW8MaxK = 131064;
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int check_w8_shape(int rows, int N, int K)
+{
+    if (rows < 0 || N < 0 || K < 0 || K % 8 != 0) return LOWBIT_E_INVALID_ARG;
+    if (rows >= kGridLimit || N >= kGridLimit || K > kW8MaxK) return LOWBIT_E_UNSUPPORTED;
+    return LOWBIT_OK;
+}
+
+int check_slots(int T, int top_k)
+{
+    if (T < 0 || top_k < 0) return LOWBIT_E_INVALID_ARG;
+    if (T >= kGridLimit || (int64_t)T * top_k >= ((int64_t)1 << 31)) return LOWBIT_E_UNSUPPORTED;
+    return LOWBIT_OK;
+}
+}  // namespace
+
+size_t lowbit_gemm_w8a8_workspace_bytes(int M, int N, int K)
+{
+    if (check_w8_shape(M, N, K) != LOWBIT_OK || M == 0 || N == 0) return 0;
+    return gemm_w8a8_workspace(M, N, K);
+}
+
+int lowbit_gemm_w8a8(int M, int N, int K, const int8_t *xq, const float *x_scale, const int8_t *wq,
+                     const float *w_scale, const float *bias, void *y, int y_dtype, void *workspace, size_t ws_bytes,
+                     void *stream)
+{
+    const int st = check_w8_shape(M, N, K);
+    if (st != LOWBIT_OK) return st;
+    if (y_dtype != LOWBIT_F16 && y_dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+    if (M == 0 || N == 0) return LOWBIT_OK;
+    if (x_scale == nullptr || w_scale == nullptr || y == nullptr || (K > 0 && (xq == nullptr || wq == nullptr)))
+        return LOWBIT_E_INVALID_ARG;
+    if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) ||
+        !aligned(y, 2))
+        return LOWBIT_E_INVALID_ARG;
+    const size_t need = gemm_w8a8_workspace(M, N, K);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LOWBIT_E_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return LOWBIT_E_INVALID_ARG;
+    const W8Args a = {xq, wq, x_scale, w_scale, bias, y, nullptr, nullptr, M, N, K, 1, M, 1, y_dtype == LOWBIT_BF16};
+    return hip_status(launch_gemm_w8a8(a, workspace, (hipStream_t)stream));
+}
+
+size_t lowbit_moe_sort_workspace_bytes(int T, int top_k, int E_local)
+{
+    if (check_slots(T, top_k) != LOWBIT_OK || E_local <= 0 || E_local > 1024) return 0;
+    return moe_sort_workspace(T * top_k, E_local);
+}
+
+int lowbit_moe_sort(const int32_t *topk_ids, int T, int top_k, int E, const int32_t *expert_map, int E_local,
+                    int32_t *row_slot, int32_t *slot_row, int32_t *expert_offsets, void *workspace, size_t ws_bytes,
+                    void *stream)
+{
+    const int st = check_slots(T, top_k);
+    if (st != LOWBIT_OK) return st;
+    if (E <= 0 || E_local <= 0) return LOWBIT_E_INVALID_ARG;
+    if (E > 1024 || E_local > 1024) return LOWBIT_E_UNSUPPORTED;
+    const int slots = T * top_k;
+    if (expert_offsets == nullptr || (slots > 0 && (topk_ids == nullptr || row_slot == nullptr || slot_row == nullptr)))
+        return LOWBIT_E_INVALID_ARG;
+    if (!aligned(topk_ids, 4) || !aligned(expert_map, 4) || !aligned(row_slot, 4) || !aligned(slot_row, 4) ||
+        !aligned(expert_offsets, 4))
+        return LOWBIT_E_INVALID_ARG;
+    const size_t need = moe_sort_workspace(slots, E_local);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LOWBIT_E_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return LOWBIT_E_INVALID_ARG;
+    return hip_status(launch_moe_sort(topk_ids, slots, E, expert_map, E_local, row_slot, slot_row, expert_offsets,
+                                      workspace, (hipStream_t)stream));
+}
+
+int lowbit_moe_permute(const void *x, const float *x_scale, int T, int top_k, int row_bytes, const int32_t *slot_row,
+                       void *xp, float *xp_scale, void *stream)
+{
+    const int st = check_slots(T, top_k);
+    if (st != LOWBIT_OK) return st;
+    if (row_bytes < 0 || row_bytes % 8 != 0 || (x_scale == nullptr) != (xp_scale == nullptr))
+        return LOWBIT_E_INVALID_ARG;
+    if (T == 0 || top_k == 0 || (row_bytes == 0 && x_scale == nullptr)) return LOWBIT_OK;
+    if (slot_row == nullptr || (row_bytes > 0 && (x == nullptr || xp == nullptr))) return LOWBIT_E_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(xp, 16) || !aligned(x_scale, 4) || !aligned(xp_scale, 4) || !aligned(slot_row, 4))
+        return LOWBIT_E_INVALID_ARG;
+    return hip_status(launch_moe_permute(x, x_scale, T, top_k, row_bytes, slot_row, xp, xp_scale, (hipStream_t)stream));
+}
+
+int lowbit_moe_unpermute(const void *yp, int dtype, const float *weights, int T, int top_k, int H,
+                         const int32_t *slot_row, void *y, void *stream)
+{
+    const int st = check_slots(T, top_k);
+    if (st != LOWBIT_OK) return st;
+    if (H < 0 || H % 8 != 0) return LOWBIT_E_INVALID_ARG;
+    if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+    if (T == 0 || H == 0) return LOWBIT_OK;
+    if (y == nullptr || (top_k > 0 && (yp == nullptr || slot_row == nullptr))) return LOWBIT_E_INVALID_ARG;
+    if (!aligned(yp, 16) || !aligned(y, 16) || !aligned(weights, 4) || !aligned(slot_row, 4))
+        return LOWBIT_E_INVALID_ARG;
+    return hip_status(launch_moe_unpermute(yp, dtype == LOWBIT_BF16, weights, T, top_k, H, slot_row, y,
+                                           (hipStream_t)stream));
+}
+
+int lowbit_moe_unpermute_backward(const void *dy, const void *yp, int dtype, const float *weights, int T, int top_k,
+                                  int H, const int32_t *slot_row, void *dyp, float *dweights, void *stream)
+{
+    const int st = check_slots(T, top_k);
+    if (st != LOWBIT_OK) return st;
+    if (H < 0 || H % 8 != 0) return LOWBIT_E_INVALID_ARG;
+    if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+    if (T == 0 || top_k == 0) return LOWBIT_OK;
+    if (weights == nullptr || dweights == nullptr || slot_row == nullptr ||
+        (H > 0 && (dy == nullptr || yp == nullptr || dyp == nullptr)))
+        return LOWBIT_E_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(yp, 16) || !aligned(dyp, 16) || !aligned(weights, 4) || !aligned(dweights, 4) ||
+        !aligned(slot_row, 4))
+        return LOWBIT_E_INVALID_ARG;
+    return hip_status(launch_moe_unpermute_backward(dy, yp, dtype == LOWBIT_BF16, weights, T, top_k, H, slot_row, dyp,
+                                                    dweights, (hipStream_t)stream));
+}
+
+int lowbit_moe_gemm_w8a8(int E, int N, int K, const int8_t *wq, const float *w_scale, const int8_t *xq,
+                         const float *x_scale, int x_rows, const int32_t *row_slot, int row_div,
+                         const int32_t *expert_offsets, int rows, void *y, int y_dtype, void *stream)
+{
+    const int st = check_w8_shape(rows, N, K);
+    if (st != LOWBIT_OK) return st;
+    if (E <= 0 || x_rows < 0) return LOWBIT_E_INVALID_ARG;
+    if (row_slot != nullptr ? row_div <= 0 || (rows > 0 && x_rows == 0) : x_rows < rows) return LOWBIT_E_INVALID_ARG;
+    if (E > 1024 || (y_dtype != LOWBIT_F16 && y_dtype != LOWBIT_BF16)) return LOWBIT_E_UNSUPPORTED;
+    if (rows == 0 || N == 0) return LOWBIT_OK;
+    if (x_scale == nullptr || w_scale == nullptr || y == nullptr || expert_offsets == nullptr ||
+        (K > 0 && (xq == nullptr || wq == nullptr)))
+        return LOWBIT_E_INVALID_ARG;
+    if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
+        !aligned(row_slot, 4) || !aligned(expert_offsets, 4) || !aligned(y, 2))
+        return LOWBIT_E_INVALID_ARG;
+    const W8Args a = {xq, wq, x_scale, w_scale, nullptr, y, row_slot, expert_offsets, rows, N, K, E, x_rows,
+                      row_slot != nullptr ? row_div : 1, y_dtype == LOWBIT_BF16};
+    return hip_status(launch_moe_gemm_w8a8(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -276,6 +276,37 @@ int lowbit_gemv_w4a8_batched_noalloc(int fmt, int M, int group_size, int count, 
                                      void *stream);
 
 /*
+ * W8A8: product of INT8 activation codes with INT8 weight codes, one scale per
+ * token and one per output channel ("Low Bit ARM kernels": 8-bit weights at
+ * the top of the bit-width table, dynamic INT8 activations, int8
+ * matrix-multiply instructions with int32 accumulation; the page names the
+ * scheme, the definition below is this library's):
+ *   y[m][n] = x_scale[m] * w_scale[n] * sum_k xq[m][k] * wq[n][k]  (+ bias[n])
+ * The sum is an exact int32; the scales and the bias are applied in fp32 (the
+ * sum by x_scale, that by w_scale), and y is rounded to nearest even into
+ * y_dtype.  Results do not depend on how the work is split: equal inputs give
+ * equal bits.  One entry point for decode and prefill.
+ *   M, N, K : any M and N below 2^24; K % 8 == 0 and K <= 131064 (the sum then
+ *             fits int32 for codes -128..127), else LOWBIT_E_UNSUPPORTED
+ *   xq      : i8  [M][K], 16-byte aligned; lowbit_quant_act_i8 makes it and x_scale
+ *   x_scale : f32 [M]
+ *   wq      : i8  [N][K], 16-byte aligned, read as it is (no packing)
+ *   w_scale : f32 [N]
+ *   bias    : f32 [N], or NULL
+ *   y       : [M][N], LOWBIT_F16 or LOWBIT_BF16 (output; must not overlap an input)
+ *   workspace : >= lowbit_gemm_w8a8_workspace_bytes(M, N, K) bytes, 256-byte
+ *             aligned (int32 partial sums where K is split over workgroups; may
+ *             be NULL when that is 0).  Nothing in it outlives the call, and it
+ *             needs no clearing; calls that may overlap need one each.
+ */
+int lowbit_gemm_w8a8(int M, int N, int K, const int8_t *xq, const float *x_scale, const int8_t *wq,
+                     const float *w_scale, const float *bias, void *y, int y_dtype,
+                     void *workspace, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of lowbit_gemm_w8a8 (0 if none is needed or the shape is invalid). */
+size_t lowbit_gemm_w8a8_workspace_bytes(int M, int N, int K);
+
+/*
  * A chain of dependent GEMV stages executed by ONE persistent launch: a whole
  * decode step (every projection of every layer) as a single submission
  * ("BaseRT" wiki chapter, limitations and approach: at batch 1 the per-command
@@ -501,6 +532,101 @@ size_t lowbit_moe_layer_workspace_bytes(int T, int top_k, int E, int H, int I, i
 int lowbit_moe_layer(const void *w13, const void *w2, int E_local, int E, int H, int I, const void *x,
                      const int32_t *topk_ids, const float *topk_weights, int T, int top_k, const int32_t *expert_map,
                      int block_m, void *y, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Tokens sorted by expert and back.  Where lowbit_moe_align lists padded slot
+ * ids for a GEMM that gathers its rows, these give rows that lie in expert
+ * order without padding, for any product, exchange or training step that
+ * works on them, and bring the results back ("vLLM PR #62759 analysis",
+ * sections "A gather" and "Expert parallelism"; the page gathers in the
+ * kernel, the sorted form is this library's).
+ *
+ * lowbit_moe_sort: the index.  Slot s = t * top_k + j is token t's j-th routed
+ * expert; its key is the local expert, expert_map[topk_ids[t][j]] (or the id
+ * itself).  Slots with an id outside [0, E) or a key outside [0, E_local) have
+ * no row.
+ *   topk_ids       : i32 [T][top_k]
+ *   expert_map     : i32 [E] global -> local expert id, -1 for experts that are
+ *                    not on this device; NULL = identity
+ *   row_slot       : i32 [T*top_k] (output) slot of each row: keys ascending,
+ *                    slots ascending within a key; T*top_k behind the last row
+ *   slot_row       : i32 [T*top_k] (output) row of each slot, -1 without one
+ *   expert_offsets : i32 [E_local+1] (output) rows of local expert e are
+ *                    [expert_offsets[e], expert_offsets[e+1])
+ *   workspace      : >= lowbit_moe_sort_workspace_bytes(T, top_k, E_local) bytes,
+ *                    256-byte aligned (may be NULL when that is 0); needs no
+ *                    clearing, calls that may overlap need one each
+ * E and E_local <= 1024, T * top_k < 2^31, else LOWBIT_E_UNSUPPORTED.  Where
+ * T * top_k is 0 the offsets are still written.
+ */
+int lowbit_moe_sort(const int32_t *topk_ids, int T, int top_k, int E, const int32_t *expert_map, int E_local,
+                    int32_t *row_slot, int32_t *slot_row, int32_t *expert_offsets, void *workspace, size_t ws_bytes,
+                    void *stream);
+
+/* Workspace bytes of lowbit_moe_sort (0 if none is needed or the shape is invalid). */
+size_t lowbit_moe_sort_workspace_bytes(int T, int top_k, int E_local);
+
+/*
+ * Rows into expert order: xp[slot_row[t*top_k + j]] = x[t] for every slot that
+ * has a row.  Rows are bytes, so INT8 codes, fp16, bf16 and fp32 all go through
+ * it; x_scale, one fp32 per row (the scales of lowbit_quant_act_i8), goes along
+ * when given.  Rows of xp behind the last one are left as they were.
+ *   x, xp             : [T] and [T*top_k] rows of row_bytes bytes, 16-byte
+ *                       aligned; row_bytes % 8 == 0; must not overlap
+ *   x_scale, xp_scale : f32 [T] and [T*top_k], both or neither
+ *   slot_row          : from lowbit_moe_sort (entries outside [0, T*top_k) count
+ *                       as slots without a row)
+ * T < 2^24 and T * top_k < 2^31, else LOWBIT_E_UNSUPPORTED (here and below).
+ * Its gradient is lowbit_moe_unpermute with weights NULL.
+ */
+int lowbit_moe_permute(const void *x, const float *x_scale, int T, int top_k, int row_bytes, const int32_t *slot_row,
+                       void *xp, float *xp_scale, void *stream);
+
+/*
+ * Rows back into token order, summed with the router's weights:
+ *   y[t][h] = RNE( sum_{j < top_k} weights[t][j] * yp[slot_row[t*top_k + j]][h] )
+ * in fp32, j ascending, over the slots that have a row (a token without any
+ * gets zeros; neither the weight nor a row of the other slots is read into the sum).
+ *   yp, dtype : [T*top_k][H] rows in expert order, LOWBIT_F16 or LOWBIT_BF16,
+ *               16-byte aligned; H % 8 == 0
+ *   weights   : f32 [T][top_k], or NULL for 1 everywhere
+ *   y         : [T][H] of the same type (output), 16-byte aligned; must not overlap yp
+ */
+int lowbit_moe_unpermute(const void *yp, int dtype, const float *weights, int T, int top_k, int H,
+                         const int32_t *slot_row, void *y, void *stream);
+
+/*
+ * Gradient of lowbit_moe_unpermute for the gradient dy of its y:
+ *   dyp[slot_row[s]][h] = RNE( weights[s] * dy[t][h] ),              s = t*top_k + j
+ *   dweights[s]         = sum_h dy[t][h] * yp[slot_row[s]][h]        (fp32; 0 without a row)
+ * Rows of dyp behind the last one are left as they were.  dyp may be yp itself
+ * (in place), no other overlap is allowed.
+ *   dy, yp, dyp, dtype : [T][H], [T*top_k][H], [T*top_k][H], as lowbit_moe_unpermute
+ *   weights, dweights  : f32 [T][top_k]
+ */
+int lowbit_moe_unpermute_backward(const void *dy, const void *yp, int dtype, const float *weights, int T, int top_k,
+                                  int H, const int32_t *slot_row, void *dyp, float *dweights, void *stream);
+
+/*
+ * The W8A8 product over rows sorted by expert (the product of lowbit_gemm_w8a8
+ * with each expert's own weights):
+ *   y[r][n] = RNE( x_scale[a] * w_scale[e][n] * sum_k xq[a][k] * wq[e][n][k] )
+ * for expert_offsets[e] <= r < expert_offsets[e+1].  Rows of y outside these
+ * ranges are left as they were.
+ *   E, N, K    : experts (<= 1024) and their shape; N and K as lowbit_gemm_w8a8
+ *   wq, w_scale: i8 [E][N][K] (16-byte aligned), f32 [E][N]
+ *   xq, x_scale: i8 [x_rows][K] (16-byte aligned), f32 [x_rows]
+ *   row_slot   : NULL where the rows of xq lie in expert order (a = r; x_rows >=
+ *                rows), or the row_slot of lowbit_moe_sort, i32 [rows], where they
+ *                do not: a = row_slot[r] / row_div, row_div being top_k when all
+ *                slots of a token read the token's row and 1 when each has its own
+ *   expert_offsets : i32 [E+1], ascending, from lowbit_moe_sort
+ *   rows       : rows of y, T*top_k (< 2^24); offsets past it are cut to it
+ *   y          : [rows][N], LOWBIT_F16 or LOWBIT_BF16 (output; must not overlap an input)
+ */
+int lowbit_moe_gemm_w8a8(int E, int N, int K, const int8_t *wq, const float *w_scale, const int8_t *xq,
+                         const float *x_scale, int x_rows, const int32_t *row_slot, int row_div,
+                         const int32_t *expert_offsets, int rows, void *y, int y_dtype, void *stream);
 
 #ifdef __cplusplus
 }
