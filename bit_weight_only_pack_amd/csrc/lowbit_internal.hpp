@@ -305,6 +305,8 @@ struct W8Args {
     void *y;                             // [rows][N], bf16 or fp16
     const int32_t *row_slot, *offsets;   // by expert: slot of each row or null, row ranges
     int rows, N, K, E, x_rows, row_div, y_bf16;
+    int splits;                          // dense: K split over this many workgroups,
+    int32_t *part;                       // their partial sums [splits][rows][N] here
 };
 // the activation row that output row r reads; a damaged table reads a wrong
 // row, never one outside the matrix
