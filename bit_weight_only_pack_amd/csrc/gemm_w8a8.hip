@@ -50,13 +50,13 @@ __device__ __forceinline__ void put8(void *y, int64_t o, const float *v, int bf1
     }
 }
 
-// 16 bytes of a row at K offset k; bytes past K (a multiple of 8) are zeros
+// 16 bytes of a row at K offset k; bytes past K (a multiple of 8, at least 8) are zeros.  No branch: many of
+// these are under way together.
 __device__ __forceinline__ i4 row16(const int8_t *row, int k, int K)
 {
-    i2 lo = {0, 0}, hi = {0, 0};
-    if (k < K) lo = *reinterpret_cast<const i2 *>(row + k);
-    if (k + 8 < K) hi = *reinterpret_cast<const i2 *>(row + k + 8);
-    return i4{lo.x, lo.y, hi.x, hi.y};
+    const i2 lo = *reinterpret_cast<const i2 *>(row + min(k, K - 8)), hi = *reinterpret_cast<const i2 *>(row + min(k + 8, K - 8));
+    const int lm = k < K ? -1 : 0, hm = k + 8 < K ? -1 : 0;
+    return i4{lo.x & lm, lo.y & lm, hi.x & hm, hi.y & hm};
 }
 
 // ---------------------------------------------------------------- streaming
@@ -374,18 +374,17 @@ void w8a8_tile_kernel(W8Args p)
 
     // load i of the wave fills LDS rows 8 (4 i + wave) .. + 7, lane -> (row, stored chunk)
     const int chunk0 = (lane & 7) ^ (((lane >> 4) + 4 * wave) & 7);
-    auto row_of = [&](int i) __attribute__((always_inline)) {
-        const int row = 8 * (kTileWaves * (i < LX ? i : i - LX) + wave) + (lane >> 3);
-        if (i >= LX) return (uint32_t)min(row, n_valid - 1) * (uint32_t)p.K;
-        const int src = min(row, m_valid - 1);
-        return (uint32_t)(MODE == EXPERTS && p.row_slot ? w8a8_source_row(p, t.first + src) : src) * (uint32_t)p.K;
-    };
     auto place = [&](uint8_t *buf, int i) __attribute__((always_inline)) {
         return buf + (i < LX ? 0 : BM * kTileK) + (kTileWaves * (i < LX ? i : i - LX) + wave) * 1024;
     };
     uint32_t off[LX + LW];
 #pragma unroll
-    for (int i = 0; i < LX + LW; ++i) off[i] = row_of(i) + chunk0 * 16;
+    for (int i = 0; i < LX + LW; ++i) {
+        const int row = 8 * (kTileWaves * (i < LX ? i : i - LX) + wave) + (lane >> 3);
+        int src = min(row, (i < LX ? m_valid : n_valid) - 1);
+        if (MODE == EXPERTS && i < LX && p.row_slot) src = w8a8_source_row(p, t.first + src);
+        off[i] = (uint32_t)src * (uint32_t)p.K + chunk0 * 16;
+    }
     // the scales and biases of the tile, on their way while K is walked; every lane loads, so that no
     // branch makes the compiler wait
     float scale[NS];
@@ -408,10 +407,17 @@ void w8a8_tile_kernel(W8Args p)
     const int full = p.K / kTileK;
     // the step that K ends inside, or an empty one that makes up a pair: bytes past K are zeros
     auto load_tail = [&](int s, uint8_t *buf) __attribute__((always_inline)) {
-#pragma unroll 1
-        for (int i = 0; i < LX + LW; ++i)
-            *reinterpret_cast<i4 *>(place(buf, i) + lane * 16) =
-                row16((i < LX ? xb : wb) + row_of(i), s * kTileK + chunk0 * 16, p.K);
+        const int k = s * kTileK + chunk0 * 16;
+#pragma unroll
+        for (int j = 0; j < LX + LW; j += 4) {
+            i4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = s * kTileK < p.K ? row16((j + i < LX ? xb : wb) + (off[j + i] - chunk0 * 16), k, p.K)
+                                        : i4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<i4 *>(place(buf, j + i) + lane * 16) = v[i];
+        }
     };
     auto load_stage = [&](int s, uint8_t *buf) __attribute__((always_inline)) {
         if (s < full) {

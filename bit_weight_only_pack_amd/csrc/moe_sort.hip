@@ -11,6 +11,8 @@
 // The gradient of permute is unpermute without weights (each token's copies
 // added up).  Nothing is added with atomics: every output has one writer and a
 // fixed order of summation, in fp32.
+#include <type_traits>
+
 #include "lowbit_internal.hpp"
 
 namespace lowbit {
@@ -19,16 +21,18 @@ namespace {
 
 // ---------------------------------------------------------------- index
 // A stable counting sort.  A workgroup of 16 waves takes one chunk of slots,
-// each wave a run of it.  Counts per (wave, key) in LDS give, scanned over
-// keys, chunks and waves, the first row of every (wave, key); a wave then walks
-// its run 64 slots at a time, where a slot's rank among the equal keys of the
-// 64 comes from ballots over the key's bits.  One workgroup is the whole sort
-// for few slots; for many, a first kernel writes every chunk's histogram and
-// each workgroup of the second one sums those of the chunks before its own.
+// each wave a run of it, 64 slots at a time.  A slot's rank among the equal
+// keys of the 64 comes from ballots over the key's bits, and one LDS add per
+// key and 64 slots gives its place among the wave's; those counts, scanned over
+// keys, chunks and waves, give the first row of every (wave, key).  One
+// workgroup is the whole sort for few slots; for many, a first kernel writes
+// every chunk's histogram and each workgroup of the second one sums those of
+// the chunks before its own.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortOneChunk = 8192;              // slots up to which one workgroup sorts
 constexpr int kSortMaxChunks = 128;
+constexpr int kSortKept = 8;                     // slots a thread keeps in registers, at most
 
 struct SortArgs {
     const int32_t *ids, *map;
@@ -36,7 +40,7 @@ struct SortArgs {
     int slots, E, E_local, chunk, bits;
 };
 
-__device__ __forceinline__ int sort_key(const SortArgs &p, int s)
+__device__ __forceinline__ int sort_key(const SortArgs &p, int64_t s)
 {
     const int id = p.ids[s];
     if (id < 0 || id >= p.E) return -1;
@@ -52,15 +56,31 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_hist_kernel(SortArgs p)
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.slots);
     for (int64_t s = begin + tid; s < end; s += kSortThreads) {
-        const int k = sort_key(p, (int)s);
+        const int k = sort_key(p, s);
         if (k >= 0) atomicAdd(&count[k], 1);
     }
     __syncthreads();
     if (tid < p.E_local) p.hist[(int64_t)blockIdx.x * p.E_local + tid] = count[tid];
 }
 
-// ONE: a single workgroup, no histograms
-template <bool ONE>
+// The place of the lane's slot among those of its key that the wave has met: `met` counts them by key
+__device__ __forceinline__ int sort_place(int k, int bits, int *met)
+{
+    const int lane = threadIdx.x & 63;
+    uint64_t same = __ballot(k >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((k >> b) & 1);
+        same &= (k >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+    int at = 0;
+    if (k >= 0 && rank == 0) at = atomicAdd(&met[k], __popcll(same));
+    return __shfl(at, k >= 0 ? __ffsll((unsigned long long)same) - 1 : lane) + rank;
+}
+
+// ONE: a single workgroup, no histograms.  R: rounds of 64 slots that a wave
+// has at most, keys and places kept in registers; 0: any number, read twice.
+template <bool ONE, int R>
 __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs p)
 {
     extern __shared__ int first[];               // [waves][E_local]: counts, then first rows
@@ -69,40 +89,57 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs p)
     const int El = p.E_local, run = p.chunk / kSortWaves;
     const int64_t base = (int64_t)blockIdx.x * p.chunk + (int64_t)wave * run;
     const int n = (int)min((int64_t)run, max((int64_t)0, (int64_t)p.slots - base));
+    constexpr int KEPT = R > 0 ? R : 1;
+    int key[KEPT], place[KEPT];
 
-    for (int i = tid; i < kSortWaves * El; i += kSortThreads) first[i] = 0;
-    __syncthreads();
-    for (int i = lane; i < n; i += 64) {
-        const int k = sort_key(p, (int)(base + i));
-        if (k >= 0) atomicAdd(&first[wave * El + k], 1);
-    }
-    __syncthreads();
-
-    // slots of key tid in all chunks, and in the chunks before this one
+    if constexpr (R > 0)
+#pragma unroll
+        for (int i = 0; i < R; ++i) key[i] = i * 64 + lane < n ? sort_key(p, base + i * 64 + lane) : -1;
     int sum = 0, pre = 0;
-    if constexpr (ONE) {
-        if (tid < El)
-            for (int w = 0; w < kSortWaves; ++w) sum += first[w * El + tid];
-    } else {
-        // groups of 2^bits threads share the chunks out
-        const int width = 1 << p.bits, groups = kSortThreads >> p.bits;
-        const int k = tid & (width - 1), g = tid >> p.bits;
+    if constexpr (!ONE) {
+        // slots of each key in all chunks and in those before this one: groups of 2^bits threads share the chunks
+        const int groups = kSortThreads >> p.bits;
+        const int k = tid & ((1 << p.bits) - 1);
         int s = 0, b = 0;
         if (k < El)
-#pragma unroll 4
-            for (int c = g; c < (int)gridDim.x; c += groups) {
+#pragma unroll 8
+            for (int c = tid >> p.bits; c < (int)gridDim.x; c += groups) {
                 const int h = p.hist[(int64_t)c * El + k];
                 s += h;
                 b += c < (int)blockIdx.x ? h : 0;
             }
         total[tid] = s;
         before[tid] = b;
-        __syncthreads();
+    }
+    for (int i = tid; i < kSortWaves * El; i += kSortThreads) first[i] = 0;
+    __syncthreads();
+    if constexpr (!ONE) {
         if (tid < El)
-            for (int q = 0; q < groups; ++q) {
-                sum += total[(q << p.bits) + tid];
-                pre += before[(q << p.bits) + tid];
+            for (int q = tid; q < kSortThreads; q += 1 << p.bits) {
+                sum += total[q];
+                pre += before[q];
             }
+    }
+    if constexpr (R > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i * 64 < n) place[i] = sort_place(key[i], p.bits, first + wave * El);
+    } else {
+        for (int i = lane; i < n; i += 64) {
+            const int k = sort_key(p, base + i);
+            if (k >= 0) atomicAdd(&first[wave * El + k], 1);
+        }
+    }
+    __syncthreads();
+
+    int count[kSortWaves];
+    if (tid < El)
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) count[w] = first[w * El + tid];
+    if constexpr (ONE) {
+        if (tid < El)
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) sum += count[w];
     }
     // exclusive scan over the keys
     int incl = sum;
@@ -114,6 +151,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs p)
     if (lane == 63) wave_sum[wave] = incl;
     __syncthreads();
     int start = incl - sum, rows = 0;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
         start += w < wave ? wave_sum[w] : 0;
         rows += wave_sum[w];
@@ -121,31 +159,29 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs p)
     if (tid < El) {
         if (blockIdx.x == 0) p.offsets[tid] = start;
         int at = start + pre;
+#pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = first[w * El + tid];
             first[w * El + tid] = at;
-            at += c;
+            at += count[w];
         }
     }
     if (blockIdx.x == 0 && tid == 0) p.offsets[El] = rows;
     __syncthreads();
 
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        const int s = (int)(base + i0 + lane);
-        const bool in = i0 + lane < n;
-        const int k = in ? sort_key(p, s) : -1;
-        uint64_t same = __ballot(k >= 0);
-        for (int b = 0; b < p.bits; ++b) {
-            const uint64_t set = __ballot((k >> b) & 1);
-            same &= (k >> b) & 1 ? set : ~set;
-        }
-        const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
-        int at = 0;
-        if (k >= 0 && rank == 0) at = atomicAdd(&first[wave * El + k], __popcll(same));
-        at = __shfl(at, k >= 0 ? __ffsll((unsigned long long)same) - 1 : lane) + rank;
-        if (in) {
-            p.slot_row[s] = k >= 0 ? at : -1;
-            if (k >= 0) p.row_slot[at] = s;
+    auto put = [&](int i, int k, int at) __attribute__((always_inline)) {
+        p.slot_row[base + i] = k >= 0 ? at : -1;
+        if (k >= 0) p.row_slot[at] = (int32_t)(base + i);
+    };
+    if constexpr (R > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i * 64 + lane < n) put(i * 64 + lane, key[i], key[i] >= 0 ? first[wave * El + key[i]] + place[i] : -1);
+    } else {
+        for (int i0 = 0; i0 < n; i0 += 64) {
+            const bool in = i0 + lane < n;
+            const int k = in ? sort_key(p, base + i0 + lane) : -1;
+            const int at = sort_place(k, p.bits, first + wave * El);
+            if (in) put(i0 + lane, k, at);
         }
     }
     // behind the last row
@@ -158,18 +194,14 @@ struct SortPlan {
 };
 SortPlan sort_plan(int slots)
 {
+    const int64_t n = slots > 0 ? slots : 1;
     SortPlan pl;
-    if (slots <= kSortOneChunk) {
-        pl.chunk = (int)round_up(slots > 0 ? slots : 1, kSortThreads);
-        pl.chunks = 1;
-        return pl;
-    }
-    const int64_t least = 4 * kSortThreads;
-    const int64_t even = round_up(((int64_t)slots + kSortMaxChunks - 1) / kSortMaxChunks, kSortThreads);
-    pl.chunk = (int)(even > least ? even : least);
-    pl.chunks = (int)(((int64_t)slots + pl.chunk - 1) / pl.chunk);
+    pl.chunk = (int)round_up(n <= kSortOneChunk ? n : (n + kSortMaxChunks - 1) / kSortMaxChunks, kSortThreads);
+    pl.chunks = (int)((n + pl.chunk - 1) / pl.chunk);
     return pl;
 }
+
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- rows
 // One token per group of `1 << shift` threads (a group walks its token's row
@@ -184,7 +216,25 @@ int row_shift(int64_t items)
     return s;
 }
 
-template <typename V>
+// Rows that no cache will hold until they are used go past it.  Measured at
+// 65536 rows of 4 KiB (us, plain / past the caches): permute 59 / 51, unpermute
+// 58 / 50, its gradient 111 / 99.
+constexpr int64_t kFarBytes = (int64_t)32 << 20;     // the L2 caches of the eight XCDs
+
+template <bool FAR, typename V>
+__device__ __forceinline__ V get_row(const V *p)
+{
+    if constexpr (FAR) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool FAR, typename V>
+__device__ __forceinline__ void put_row(V *p, V v)
+{
+    if constexpr (FAR) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
+template <bool FAR, typename V>
 __global__ __launch_bounds__(kRowThreads)
 void moe_permute_kernel(const V *x, const float *x_scale, int T, int top_k, int items, int shift,
                         const int32_t *slot_row, V *xp, float *xp_scale)
@@ -198,7 +248,7 @@ void moe_permute_kernel(const V *x, const float *x_scale, int T, int top_k, int 
         const V v = x[t * items + c];
         for (int j = 0; j < top_k; ++j) {
             const int r = rows[j];
-            if (r >= 0 && r < limit) xp[(int64_t)r * items + c] = v;
+            if (r >= 0 && r < limit) put_row<FAR>(xp + (int64_t)r * items + c, v);
         }
     }
     if (x_scale != nullptr && c0 == 0) {
@@ -214,7 +264,10 @@ template <bool BF16> struct Elem;
 template <> struct Elem<true> { typedef __bf16 v8 __attribute__((ext_vector_type(8))); typedef __bf16 t; };
 template <> struct Elem<false> { typedef _Float16 v8 __attribute__((ext_vector_type(8))); typedef _Float16 t; };
 
-template <bool BF16>
+// Slots whose rows a thread has under way together
+constexpr int kRowBatch = 8;
+
+template <bool FAR, bool BF16>
 __global__ __launch_bounds__(kRowThreads)
 void moe_unpermute_kernel(const typename Elem<BF16>::v8 *yp, const float *w, int T, int top_k, int items, int shift,
                           const int32_t *slot_row, typename Elem<BF16>::v8 *y)
@@ -227,13 +280,24 @@ void moe_unpermute_kernel(const typename Elem<BF16>::v8 *yp, const float *w, int
     const int64_t limit = (int64_t)T * top_k;
     for (int c = threadIdx.x & ((1 << shift) - 1); c < items; c += 1 << shift) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < top_k; ++j) {
-            const int r = rows[j];
-            if (r < 0 || r >= limit) continue;
-            const float wj = w ? w[t * top_k + j] : 1.f;
-            const v8 v = yp[(int64_t)r * items + c];
+        for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
+            int r[kRowBatch];
+            v8 v[kRowBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(wj, (float)v[i], acc[i]);
+            for (int j = 0; j < kRowBatch; ++j) {
+                r[j] = j0 + j < top_k ? rows[j0 + j] : -1;
+                if (r[j] >= limit) r[j] = -1;
+            }
+#pragma unroll
+            for (int j = 0; j < kRowBatch; ++j)
+                if (r[j] >= 0) v[j] = get_row<FAR>(yp + (int64_t)r[j] * items + c);
+#pragma unroll
+            for (int j = 0; j < kRowBatch; ++j)
+                if (r[j] >= 0) {
+                    const float wj = w ? w[t * top_k + j0 + j] : 1.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(wj, (float)v[j][i], acc[i]);
+                }
         }
         v8 o;
 #pragma unroll
@@ -242,41 +306,62 @@ void moe_unpermute_kernel(const typename Elem<BF16>::v8 *yp, const float *w, int
     }
 }
 
-// One workgroup per token
-template <bool BF16>
-__global__ __launch_bounds__(kRowThreads)
+// One workgroup of NW waves per token, kRowBatch slots at a time: their rows are read and written in one pass over
+// dy, and their sums cross the lanes together.
+template <bool FAR, bool BF16, int NW>
+__global__ __launch_bounds__(NW * 64)
 void moe_unpermute_backward_kernel(const typename Elem<BF16>::v8 *dy, const typename Elem<BF16>::v8 *yp,
                                    const float *w, int T, int top_k, int items, const int32_t *slot_row,
                                    typename Elem<BF16>::v8 *dyp, float *dw)
 {
     typedef typename Elem<BF16>::v8 v8;
     typedef typename Elem<BF16>::t T1;
-    __shared__ float part[kRowThreads / 64];
+    __shared__ float part[NW][kRowBatch];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int j = 0; j < top_k; ++j) {
-        const int64_t s = t * top_k + j;
-        const int r = slot_row[s];
-        const bool has = r >= 0 && r < (int64_t)T * top_k;
-        const float wj = w[s];
-        float dot = 0.f;
-        if (has)
-            for (int c = tid; c < items; c += kRowThreads) {
-                const v8 g = dy[t * items + c], v = yp[(int64_t)r * items + c];
-                v8 o;
+    for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
+        int r[kRowBatch];
+        float wj[kRowBatch], dot[kRowBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot = __builtin_fmaf((float)g[i], (float)v[i], dot);
-                    o[i] = (T1)(wj * (float)g[i]);
+        for (int j = 0; j < kRowBatch; ++j) {
+            const int64_t s = t * top_k + j0 + j;
+            r[j] = j0 + j < top_k ? slot_row[s] : -1;
+            if (r[j] >= (int64_t)T * top_k) r[j] = -1;
+            wj[j] = r[j] >= 0 ? w[s] : 0.f;
+            dot[j] = 0.f;
+        }
+        for (int c = tid; c < items; c += NW * 64) {
+            const v8 g = dy[t * items + c];
+            v8 v[kRowBatch];
+#pragma unroll
+            for (int j = 0; j < kRowBatch; ++j)
+                if (r[j] >= 0) v[j] = get_row<FAR>(yp + (int64_t)r[j] * items + c);
+#pragma unroll
+            for (int j = 0; j < kRowBatch; ++j)
+                if (r[j] >= 0) {
+                    v8 o;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot[j] = __builtin_fmaf((float)g[i], (float)v[j][i], dot[j]);
+                        o[i] = (T1)(wj[j] * (float)g[i]);
+                    }
+                    put_row<FAR>(dyp + (int64_t)r[j] * items + c, o);
                 }
-                dyp[(int64_t)r * items + c] = o;
-            }
+        }
+        if (j0 > 0) __syncthreads();                  // the sums of the slots before are read
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
-        if (lane == 0) part[wave] = dot;
+        for (int j = 0; j < kRowBatch; ++j) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o);
+            if (lane == 0) part[wave][j] = dot[j];
+        }
         __syncthreads();
-        if (tid == 0) dw[s] = has ? (part[0] + part[1]) + (part[2] + part[3]) : 0.f;
-        __syncthreads();
+        if (tid < kRowBatch && j0 + tid < top_k) {
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < NW; ++q) s += part[q][tid];
+            dw[t * top_k + j0 + tid] = s;
+        }
     }
 }
 
@@ -297,71 +382,80 @@ hipError_t launch_moe_sort(const int32_t *topk_ids, int slots, int E, const int3
     const SortArgs a = {topk_ids, expert_map, row_slot, slot_row, expert_offsets, static_cast<int32_t *>(ws),
                         slots, E, E_local, pl.chunk, bits};
     const size_t lds = (size_t)kSortWaves * E_local * sizeof(int);
-    if (pl.chunks == 1) {
-        moe_sort_kernel<true><<<1, kSortThreads, lds, s>>>(a);
-    } else {
+    auto launch = [&](auto kernel) {
+        if (E_local > 800) {                          // with the fixed arrays more than 64 KiB: asked for
+            const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                     (int)lds);
+            if (e != hipSuccess) return e;
+        }
+        kernel<<<pl.chunks, kSortThreads, lds, s>>>(a);
+        return hipGetLastError();
+    };
+    if (pl.chunks > 1) {
         moe_sort_hist_kernel<<<pl.chunks, kSortThreads, 0, s>>>(a);
-        moe_sort_kernel<false><<<pl.chunks, kSortThreads, lds, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    const int rounds = pl.chunk / kSortThreads;
+    if (pl.chunks == 1) return rounds == 1 ? launch(moe_sort_kernel<true, 1>) : launch(moe_sort_kernel<true, kSortKept>);
+    if (rounds == 1) return launch(moe_sort_kernel<false, 1>);
+    return rounds <= kSortKept ? launch(moe_sort_kernel<false, kSortKept>) : launch(moe_sort_kernel<false, 0>);
 }
 
 hipError_t launch_moe_permute(const void *x, const float *x_scale, int T, int top_k, int row_bytes,
                               const int32_t *slot_row, void *xp, float *xp_scale, hipStream_t s)
 {
-    const bool wide = row_bytes % 16 == 0;
+    const bool wide = row_bytes % 16 == 0, far = (int64_t)T * top_k * row_bytes > kFarBytes;
     const int items = row_bytes / (wide ? 16 : 8), shift = row_shift(items);
     const unsigned blocks = (unsigned)(((int64_t)T + (256 >> shift) - 1) >> (8 - shift));
-    if (wide)
-        moe_permute_kernel<u4><<<blocks, kRowThreads, 0, s>>>(static_cast<const u4 *>(x), x_scale, T, top_k, items,
-                                                              shift, slot_row, static_cast<u4 *>(xp), xp_scale);
-    else
-        moe_permute_kernel<uint2><<<blocks, kRowThreads, 0, s>>>(static_cast<const uint2 *>(x), x_scale, T, top_k,
-                                                                 items, shift, slot_row, static_cast<uint2 *>(xp),
-                                                                 xp_scale);
-    return hipGetLastError();
+    auto launch = [&](auto kernel, auto item) {
+        typedef decltype(item) V;
+        kernel<<<blocks, kRowThreads, 0, s>>>(static_cast<const V *>(x), x_scale, T, top_k, items, shift, slot_row,
+                                              static_cast<V *>(xp), xp_scale);
+        return hipGetLastError();
+    };
+    if (wide) return far ? launch(moe_permute_kernel<true, u4>, u4{}) : launch(moe_permute_kernel<false, u4>, u4{});
+    return far ? launch(moe_permute_kernel<true, u2>, u2{}) : launch(moe_permute_kernel<false, u2>, u2{});
 }
-
-namespace {
-template <bool BF16>
-void unpermute(const void *yp, const float *w, int T, int top_k, int items, const int32_t *slot_row, void *y,
-               hipStream_t s)
-{
-    typedef typename Elem<BF16>::v8 v8;
-    const int shift = row_shift(items);
-    const unsigned blocks = (unsigned)(((int64_t)T + (256 >> shift) - 1) >> (8 - shift));
-    moe_unpermute_kernel<BF16><<<blocks, kRowThreads, 0, s>>>(static_cast<const v8 *>(yp), w, T, top_k, items, shift,
-                                                              slot_row, static_cast<v8 *>(y));
-}
-template <bool BF16>
-void unpermute_backward(const void *dy, const void *yp, const float *w, int T, int top_k, int items,
-                        const int32_t *slot_row, void *dyp, float *dw, hipStream_t s)
-{
-    typedef typename Elem<BF16>::v8 v8;
-    moe_unpermute_backward_kernel<BF16><<<(unsigned)T, kRowThreads, 0, s>>>(
-        static_cast<const v8 *>(dy), static_cast<const v8 *>(yp), w, T, top_k, items, slot_row, static_cast<v8 *>(dyp),
-        dw);
-}
-}  // namespace
 
 hipError_t launch_moe_unpermute(const void *yp, int bf16, const float *w, int T, int top_k, int H,
                                 const int32_t *slot_row, void *y, hipStream_t s)
 {
-    if (bf16)
-        unpermute<true>(yp, w, T, top_k, H / 8, slot_row, y, s);
-    else
-        unpermute<false>(yp, w, T, top_k, H / 8, slot_row, y, s);
-    return hipGetLastError();
+    const bool far = (int64_t)T * top_k * H * 2 > kFarBytes;
+    const int items = H / 8, shift = row_shift(items);
+    const unsigned blocks = (unsigned)(((int64_t)T + (256 >> shift) - 1) >> (8 - shift));
+    auto launch = [&](auto kernel, auto item) {
+        typedef decltype(item) v8;
+        kernel<<<blocks, kRowThreads, 0, s>>>(static_cast<const v8 *>(yp), w, T, top_k, items, shift, slot_row,
+                                              static_cast<v8 *>(y));
+        return hipGetLastError();
+    };
+    typedef Elem<true>::v8 b8;
+    if (bf16) return far ? launch(moe_unpermute_kernel<true, true>, b8{}) : launch(moe_unpermute_kernel<false, true>, b8{});
+    return far ? launch(moe_unpermute_kernel<true, false>, h8{}) : launch(moe_unpermute_kernel<false, false>, h8{});
 }
 
 hipError_t launch_moe_unpermute_backward(const void *dy, const void *yp, int bf16, const float *w, int T, int top_k,
                                          int H, const int32_t *slot_row, void *dyp, float *dw, hipStream_t s)
 {
-    if (bf16)
-        unpermute_backward<true>(dy, yp, w, T, top_k, H / 8, slot_row, dyp, dw, s);
-    else
-        unpermute_backward<false>(dy, yp, w, T, top_k, H / 8, slot_row, dyp, dw, s);
-    return hipGetLastError();
+    const bool far = (int64_t)T * top_k * H * 2 > kFarBytes;
+    const int items = H / 8;
+    auto launch = [&](auto kernel, int waves, auto item) {
+        typedef decltype(item) v8;
+        kernel<<<(unsigned)T, waves * 64, 0, s>>>(static_cast<const v8 *>(dy), static_cast<const v8 *>(yp), w, T, top_k,
+                                                  items, slot_row, static_cast<v8 *>(dyp), dw);
+        return hipGetLastError();
+    };
+    auto pick = [&](auto b, auto item) {
+        constexpr bool B = decltype(b)::value;
+        if (items <= 64)                              // one wave has the whole row
+            return far ? launch(moe_unpermute_backward_kernel<true, B, 1>, 1, item)
+                       : launch(moe_unpermute_backward_kernel<false, B, 1>, 1, item);
+        return far ? launch(moe_unpermute_backward_kernel<true, B, 4>, 4, item)
+                   : launch(moe_unpermute_backward_kernel<false, B, 4>, 4, item);
+    };
+    typedef Elem<true>::v8 b8;
+    return bf16 ? pick(std::true_type{}, b8{}) : pick(std::false_type{}, h8{});
 }
 
 }  // namespace lowbit

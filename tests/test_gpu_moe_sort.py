@@ -25,6 +25,7 @@ def _map(rng, E, El):
     (1, 1, 1, 1), (1, 8, 128, 128), (3, 2, 5, 5), (37, 8, 128, 128), (64, 1, 2, 2), (129, 6, 1024, 1024),
     (1000, 8, 60, 17), (1024, 8, 128, 128), (1025, 8, 128, 128),      # the last size of one workgroup, and one more
     (5000, 7, 1000, 333), (16384, 8, 128, 128), (70001, 9, 3, 2), (9000, 1, 1024, 1024),
+    (200, 5, 900, 801), (150000, 8, 40, 40),                          # past the slots that stay in registers
 ])
 def test_sort_bitexact(T, top_k, E, El):
     rng = np.random.default_rng(T + E)
