@@ -329,7 +329,11 @@ __global__ __launch_bounds__(kTileWaves * 64, 1)
 void w8a8_tile_kernel(W8Args p)
 {
     constexpr int NST = kStages<BM, BN>;
-    constexpr int TC = BN / 64, TT = BM / 64;         // 32-wide blocks of a wave: channels, tokens
+    // 64 x 64: each wave has the whole tile and a quarter of every 128 bytes of K, so that no operand is read
+    // from LDS twice; otherwise each has a quarter of the tile.
+    constexpr bool KW = BM * BN == 64 * 64;
+    constexpr int NK = KW ? 1 : 4;                    // 32-byte pieces of a step that a wave multiplies
+    constexpr int TC = KW ? 2 : BN / 64, TT = KW ? 2 : BM / 64;   // 32-wide blocks of a wave: channels, tokens
     constexpr int LX = BM / 8 / kTileWaves, LW = BN / 8 / kTileWaves;   // LDS-direct loads of a wave per stage
     constexpr int STAGE = (BM + BN) * kTileK;
     __shared__ __attribute__((aligned(1024))) uint8_t stages[NST * STAGE];
@@ -338,7 +342,7 @@ void w8a8_tile_kernel(W8Args p)
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wt = wave & 1, wc = wave >> 1;
+    const int wt = KW ? 0 : wave & 1, wc = KW ? 0 : wave >> 1;
     W8Tile t;
     int s0 = 0, s1 = (p.K + 2 * kTileK - 1) / (2 * kTileK) * 2, split = 0;   // steps, in pairs
     if constexpr (MODE == EXPERTS) {
@@ -437,10 +441,10 @@ void w8a8_tile_kernel(W8Args p)
     };
 
     // operand addresses: 32-row block, K chunk 2 k + lane / 32
-    int at[4];
+    int at[NK];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        at[k] = (lane & 31) * kTileK + ((2 * k + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
+    for (int k = 0; k < NK; ++k)
+        at[k] = (lane & 31) * kTileK + ((2 * (KW ? wave : k) + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
     auto token = [&](const uint8_t *buf, int b, int k) __attribute__((always_inline)) {
         return *reinterpret_cast<const i4 *>(buf + (wt * TT + b) * 32 * kTileK + at[k]);
     };
@@ -471,9 +475,9 @@ void w8a8_tile_kernel(W8Args p)
         else
             sync(std::integral_constant<int, 0>{});
         uint8_t *const buf0 = stages;
-        i4 wf[2][TC][4], xf[P2][kRoom ? TT : 3][4];
+        i4 wf[2][TC][NK], xf[P2][kRoom ? TT : 3][NK];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < NK; ++k) {
 #pragma unroll
             for (int c = 0; c < TC; ++c) wf[0][c][k] = channel(buf0, c, k);
 #pragma unroll
@@ -497,8 +501,8 @@ void w8a8_tile_kernel(W8Args p)
                     for (int c = 0; c < TC; ++c) {
                         // this block's share of the next step's operands and of the loads two steps ahead
 #pragma unroll
-                        for (int f = 0; f < (TC + TT) * 4; ++f)
-                            if (f * TC * TT / ((TC + TT) * 4) == b * TC + c) {
+                        for (int f = 0; f < (TC + TT) * NK; ++f)
+                            if (f * TC * TT / ((TC + TT) * NK) == b * TC + c) {
                                 const int fk = f / (TC + TT), fi = f % (TC + TT);
                                 if (fi < TC)
                                     wf[Q][fi][fk] = channel(nxt, fi, fk);
@@ -511,7 +515,7 @@ void w8a8_tile_kernel(W8Args p)
                                 if (i * TC * TT / (LX + LW) == b * TC + c) load_one(s + NST, cur, i);
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < NK; ++k)
                             acc[c][b] =
                                 __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[P][c][k], xf[P][b][k], acc[c][b], 0, 0, 0);
                         __builtin_amdgcn_sched_barrier(0);
@@ -568,11 +572,10 @@ void w8a8_tile_kernel(W8Args p)
     // A lane holds token lane % 32 of a block and channels 8 g + 4 (lane / 32) + 0 .. 3.  32 tokens at a
     // time go through LDS (16-byte chunk c of row r at c ^ r) and come back as rows, eight channels a lane,
     // in a loop: unrolled, this code is so long that fetching it takes longer than running it.
-    constexpr int CW = BN / 2, CHUNKS = CW / 4;       // channels of a wave, their chunks in a row
-    static_assert(kTileWaves * 32 * CW * 4 <= NST * STAGE, "the waves' rows fit");
-    uint8_t *mine = stages + wave * (32 * CW * 4);
-    const int c8 = lane % (CW / 8) * 8, r0 = lane / (CW / 8), n = wc * CW + c8;
-    constexpr int RSTEP = 64 / (CW / 8);
+    constexpr int CW = KW ? BN : BN / 2, CHUNKS = CW / 4;   // channels of a wave, their chunks in a row
+    constexpr int REGION = 32 * CW * 4;
+    static_assert(kTileWaves * REGION * (KW ? TT : 1) <= NST * STAGE, "the waves' rows fit");
+    const int c8 = lane % (CW / 8) * 8, n = wc * CW + c8;
     f4 ws[2], bs[2];
     if constexpr (MODE != SPLIT)
 #pragma unroll
@@ -582,49 +585,72 @@ void w8a8_tile_kernel(W8Args p)
         }
     const bool wide = MODE == SPLIT ? (p.N & 3) == 0
                                     : (p.N & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
-#pragma unroll
-    for (int b = 0; b < TT; ++b) {
+    auto stash = [&](int b, uint8_t *region) __attribute__((always_inline)) {
 #pragma unroll
         for (int c = 0; c < TC; ++c)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<i4 *>(mine + (lane & 31) * (CW * 4) +
+                *reinterpret_cast<i4 *>(region + (lane & 31) * (CW * 4) +
                                         (((c * 8 + 2 * g + (lane >> 5)) ^ (lane & (CHUNKS - 1))) * 16)) =
                     i4{acc[c][b][4 * g], acc[c][b][4 * g + 1], acc[c][b][4 * g + 2], acc[c][b][4 * g + 3]};
-        const int tok0 = (wt * TT + b) * 32, rows = min(32, m_valid - tok0);
-        const int64_t row0 = (int64_t)(t.first + tok0) * p.N + t.n0 + n;
-#pragma unroll 4
-        for (int r = r0; r < 32; r += RSTEP) {
-            i4 v[2];
+    };
+    auto fetch = [&](const uint8_t *region, int r, int h) __attribute__((always_inline)) {
+        return *reinterpret_cast<const i4 *>(region + r * (CW * 4) + (((c8 / 4 + h) ^ (r & (CHUNKS - 1))) * 16));
+    };
+    auto emit = [&](int tok, const i4 *v) __attribute__((always_inline)) {
+        if (tok >= m_valid) return;
+        const int64_t o = (int64_t)(t.first + tok) * p.N + t.n0 + n;
+        if constexpr (MODE == SPLIT) {
+            int32_t *to = p.part + (int64_t)split * p.rows * p.N + o;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                v[h] = *reinterpret_cast<const i4 *>(mine + r * (CW * 4) + (((c8 / 4 + h) ^ (r & (CHUNKS - 1))) * 16));
-            if (r >= rows) continue;
-            const int64_t o = row0 + (int64_t)r * p.N;
-            if constexpr (MODE == SPLIT) {
-                int32_t *to = p.part + (int64_t)split * p.rows * p.N + o;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (wide) {
-                        if (n + 4 * h < n_valid) *reinterpret_cast<i4 *>(to + 4 * h) = v[h];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n + 4 * h + i < n_valid) to[4 * h + i] = v[h][i];
-                    }
-                }
-            } else {
-                const float xs = sc[tok0 + r];
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = (float)v[i / 4][i % 4] * xs * ws[i / 4][i % 4] + bs[i / 4][i % 4];
+            for (int h = 0; h < 2; ++h) {
                 if (wide) {
-                    if (n < n_valid) put8(p.y, o, f, p.y_bf16);
+                    if (n + 4 * h < n_valid) *reinterpret_cast<i4 *>(to + 4 * h) = v[h];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (n + i < n_valid) put(p.y, o + i, f[i], p.y_bf16);
+                    for (int i = 0; i < 4; ++i)
+                        if (n + 4 * h + i < n_valid) to[4 * h + i] = v[h][i];
                 }
+            }
+        } else {
+            const float xs = sc[tok];
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = (float)v[i / 4][i % 4] * xs * ws[i / 4][i % 4] + bs[i / 4][i % 4];
+            if (wide) {
+                if (n < n_valid) put8(p.y, o, f, p.y_bf16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (n + i < n_valid) put(p.y, o + i, f[i], p.y_bf16);
+            }
+        }
+    };
+    if constexpr (KW) {
+        // every wave's sums of the tile; each then adds up and finishes 8 of a block's 32 rows
+#pragma unroll
+        for (int b = 0; b < TT; ++b) stash(b, stages + (wave * TT + b) * REGION);
+        sync(std::integral_constant<int, 0>{});
+#pragma unroll
+        for (int b = 0; b < TT; ++b) {
+            const int r = wave * 8 + lane / 8;
+            i4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int q = 0; q < kTileWaves; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) v[h] += fetch(stages + (q * TT + b) * REGION, r, h);
+            emit(b * 32 + r, v);
+        }
+    } else {
+        uint8_t *mine = stages + wave * REGION;
+        constexpr int RSTEP = 64 / (CW / 8);
+#pragma unroll
+        for (int b = 0; b < TT; ++b) {
+            stash(b, mine);
+#pragma unroll 4
+            for (int r = lane / (CW / 8); r < 32; r += RSTEP) {
+                const i4 v[2] = {fetch(mine, r, 0), fetch(mine, r, 1)};
+                emit((wt * TT + b) * 32 + r, v);
             }
         }
     }
@@ -727,7 +753,7 @@ W8Plan w8_plan(int rows, int N, int K)
         int size;
         double ends, step, least;                     // microseconds
     };
-    constexpr Cost kCosts[] = {{64, 4.0, 0.23, 0.22}, {128, 6.0, 0.56, 0.56}, {256, 14.0, 1.6, 1.6}};
+    constexpr Cost kCosts[] = {{64, 4.0, 0.25, 0.2}, {128, 6.0, 0.56, 0.56}, {256, 14.0, 1.6, 1.6}};
     const int pairs = (K + 2 * kTileK - 1) / (2 * kTileK);
     W8Plan best = {64, 1, 0};
     double time = -1.0;

@@ -234,6 +234,19 @@ __device__ __forceinline__ void put_row(V *p, V v)
     else *p = v;
 }
 
+// Slots whose rows a thread has under way together
+constexpr int kRowBatch = 8;
+
+// rows of slots j0 .. j0 + kRowBatch - 1 of a token, -1 where there is none
+__device__ __forceinline__ void batch_rows(const int32_t *rows, int j0, int top_k, int64_t limit, int (&r)[kRowBatch])
+{
+#pragma unroll
+    for (int j = 0; j < kRowBatch; ++j) r[j] = rows[min(j0 + j, top_k - 1)];
+#pragma unroll
+    for (int j = 0; j < kRowBatch; ++j)
+        if (j0 + j >= top_k || r[j] >= limit) r[j] = -1;
+}
+
 template <bool FAR, typename V>
 __global__ __launch_bounds__(kRowThreads)
 void moe_permute_kernel(const V *x, const float *x_scale, int T, int top_k, int items, int shift,
@@ -241,31 +254,28 @@ void moe_permute_kernel(const V *x, const float *x_scale, int T, int top_k, int 
 {
     const int64_t t = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
     if (t >= T) return;
-    const int32_t *rows = slot_row + t * top_k;
-    const int64_t limit = (int64_t)T * top_k;
     const int c0 = threadIdx.x & ((1 << shift) - 1);
-    for (int c = c0; c < items; c += 1 << shift) {
-        const V v = x[t * items + c];
-        for (int j = 0; j < top_k; ++j) {
-            const int r = rows[j];
-            if (r >= 0 && r < limit) put_row<FAR>(xp + (int64_t)r * items + c, v);
+    const bool scaled = x_scale != nullptr && c0 == 0;
+    const float scale = scaled ? x_scale[t] : 0.f;
+    for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
+        int r[kRowBatch];
+        batch_rows(slot_row + t * top_k, j0, top_k, (int64_t)T * top_k, r);
+        for (int c = c0; c < items; c += 1 << shift) {
+            const V v = x[t * items + c];
+#pragma unroll
+            for (int j = 0; j < kRowBatch; ++j)
+                if (r[j] >= 0) put_row<FAR>(xp + (int64_t)r[j] * items + c, v);
         }
-    }
-    if (x_scale != nullptr && c0 == 0) {
-        const float v = x_scale[t];
-        for (int j = 0; j < top_k; ++j) {
-            const int r = rows[j];
-            if (r >= 0 && r < limit) xp_scale[r] = v;
-        }
+        if (scaled)
+#pragma unroll
+            for (int j = 0; j < kRowBatch; ++j)
+                if (r[j] >= 0) xp_scale[r[j]] = scale;
     }
 }
 
 template <bool BF16> struct Elem;
 template <> struct Elem<true> { typedef __bf16 v8 __attribute__((ext_vector_type(8))); typedef __bf16 t; };
 template <> struct Elem<false> { typedef _Float16 v8 __attribute__((ext_vector_type(8))); typedef _Float16 t; };
-
-// Slots whose rows a thread has under way together
-constexpr int kRowBatch = 8;
 
 template <bool FAR, bool BF16>
 __global__ __launch_bounds__(kRowThreads)
@@ -276,18 +286,12 @@ void moe_unpermute_kernel(const typename Elem<BF16>::v8 *yp, const float *w, int
     typedef typename Elem<BF16>::t T1;
     const int64_t t = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
     if (t >= T) return;
-    const int32_t *rows = slot_row + t * top_k;
-    const int64_t limit = (int64_t)T * top_k;
     for (int c = threadIdx.x & ((1 << shift) - 1); c < items; c += 1 << shift) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
             int r[kRowBatch];
             v8 v[kRowBatch];
-#pragma unroll
-            for (int j = 0; j < kRowBatch; ++j) {
-                r[j] = j0 + j < top_k ? rows[j0 + j] : -1;
-                if (r[j] >= limit) r[j] = -1;
-            }
+            batch_rows(slot_row + t * top_k, j0, top_k, (int64_t)T * top_k, r);
 #pragma unroll
             for (int j = 0; j < kRowBatch; ++j)
                 if (r[j] >= 0) v[j] = get_row<FAR>(yp + (int64_t)r[j] * items + c);
@@ -322,12 +326,10 @@ void moe_unpermute_backward_kernel(const typename Elem<BF16>::v8 *dy, const type
     for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
         int r[kRowBatch];
         float wj[kRowBatch], dot[kRowBatch];
+        batch_rows(slot_row + t * top_k, j0, top_k, (int64_t)T * top_k, r);
 #pragma unroll
         for (int j = 0; j < kRowBatch; ++j) {
-            const int64_t s = t * top_k + j0 + j;
-            r[j] = j0 + j < top_k ? slot_row[s] : -1;
-            if (r[j] >= (int64_t)T * top_k) r[j] = -1;
-            wj[j] = r[j] >= 0 ? w[s] : 0.f;
+            wj[j] = w[t * top_k + min(j0 + j, top_k - 1)];
             dot[j] = 0.f;
         }
         for (int c = tid; c < items; c += NW * 64) {
@@ -351,6 +353,7 @@ void moe_unpermute_backward_kernel(const typename Elem<BF16>::v8 *dy, const type
         if (j0 > 0) __syncthreads();                  // the sums of the slots before are read
 #pragma unroll
         for (int j = 0; j < kRowBatch; ++j) {
+            if (j0 + j >= top_k) break;
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o);
             if (lane == 0) part[wave][j] = dot[j];
