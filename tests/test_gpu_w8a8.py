@@ -49,7 +49,11 @@ def gemm(xq, xs, wq, ws, bias, dt, y=None, stream=None):
 SHAPES = [
     # decode: one token, few tokens, ragged channels, K with and without a tail below 16 and 64
     (1, 1, 8), (1, 16, 64), (1, 300, 1056), (2, 33, 24), (3, 64, 136), (5, 1000, 4104), (8, 48, 14336), (15, 17, 72),
-    (16, 4096, 1024), (1, 4096, 4096),
+    (16, 4096, 1024), (1, 4096, 4096), (2, 20, 3000), (11, 35, 4200), (16, 24, 4224), (7, 18, 9000),
+    # few rows and many channels
+    (4, 12288, 4096), (9, 13001, 2200), (16, 12300, 4216), (5, 12295, 4224),
+    # K shared between workgroups
+    (17, 64, 9000), (40, 200, 14336), (64, 1000, 4104), (100, 131, 6664),
     # around the row counts where a tile ends
     (17, 40, 264), (31, 129, 512), (32, 128, 128), (33, 257, 200), (63, 64, 2048), (64, 64, 64), (65, 130, 1032),
     (100, 1023, 520), (127, 255, 8), (128, 256, 128), (129, 257, 136), (200, 96, 7176),
@@ -71,6 +75,23 @@ def test_gemm_parity(M, N, K, dt, bias):
         y64, step = product64(xq, xs, wq, ws, b)
     y = gemm(dev(xq), dev(xs), dev(wq), dev(ws), None if b is None else dev(b), dt)
     assert_rounded(y, y64, step, DT[dt][1], "M=%d N=%d K=%d" % (M, N, K))
+
+
+@pytest.mark.parametrize("M,N,K", [(4090, 4095, 8200), (4096, 4096, 4096), (700, 9000, 520)])
+def test_gemm_large(M, N, K):
+    """Sizes of the widest tiles, ragged and not; the 64-bit product on the GPU, all values."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    xq = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    wq = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    xs = torch.rand(M, device="cuda", generator=g) * 0.01
+    ws = torch.rand(N, device="cuda", generator=g) * 0.01
+    bias = torch.randn(N, device="cuda", generator=g)
+    y = gemm(xq, xs, wq, ws, bias, "bf16").double()
+    p64 = torch.mm(xq.double(), wq.double().t()) * xs.double()[:, None] * ws.double()[None, :]
+    y64 = p64 + bias.double()
+    step = 4.01 * U32 * (p64.abs() + bias.double().abs())
+    bound = 2.0 ** -8 * (y64.abs() + step) + step + 2.0 ** -134
+    assert bool(((y - y64).abs() <= bound).all())
 
 
 @pytest.mark.parametrize("M", [1, 40, 300])
@@ -210,6 +231,7 @@ def run_experts(xq, xs, wq, ws, row_slot, row_div, offs, rows, dt, stream=None):
     (300, 2, 8, 260, 520, 0.7), (300, 4, 16, 100, 1032, 3.0),      # ragged experts; most rows with a few experts
     (700, 2, 5, 513, 136, 0.7), (1500, 1, 3, 300, 264, 2.0),
     (5, 4, 1000, 16, 64, 0.7),                                     # most experts empty
+    (400, 2, 2, 300, 4104, 0.0), (90, 2, 6, 70, 4232, 0.7), (3, 3, 3, 50, 9000, 0.7),      # long K
 ])
 @pytest.mark.parametrize("gather,dt", [(True, "bf16"), (False, "f16")])
 def test_experts_parity(T, top_k, E, N, K, skew, gather, dt):
@@ -248,6 +270,29 @@ def test_experts_rows_outside_stay(T):
     cut = last - 7                                   # fewer rows than the table names
     y = run_experts(dev(xq), dev(xs), dev(wq), dev(ws), row_slot, top_k, offs, cut, "bf16")
     assert_rounded(y, y64[:cut], step[:cut], torch.bfloat16)
+
+
+@pytest.mark.parametrize("x_rows", [262160, 524300])
+@pytest.mark.parametrize("rows", [10, 100, 600])
+def test_experts_gather_past_2_31(x_rows, rows):
+    """Gathered rows whose offsets pass 2^31 and 2^32 bytes, among them the first and the last ones."""
+    E, N, K = 4, 40, 8200
+    g = torch.Generator(device="cuda").manual_seed(7)
+    xq = torch.empty((x_rows, K), dtype=torch.int8, device="cuda")
+    for lo in range(0, x_rows, 1 << 16):
+        xq[lo:lo + (1 << 16)].random_(-128, 128, generator=g)
+    wq = torch.randint(-128, 128, (E, N, K), dtype=torch.int8, device="cuda", generator=g)
+    xs = torch.rand(x_rows, device="cuda", generator=g) * 0.01
+    ws = torch.rand(E, N, device="cuda", generator=g) * 0.01
+    rng = np.random.default_rng(rows)
+    src = rng.integers(0, x_rows, rows)
+    src[:2], src[-2:] = [0, x_rows - 1], [x_rows - 1, x_rows - 2]
+    offs = np.array([0, rows // 3, rows // 3, rows - 5, rows], np.int32)
+    y = run_experts(xq, xs, wq, ws, dev((3 * src + 1).astype(np.int32)), 3, dev(offs), rows, "bf16")
+    t = torch.from_numpy(src).cuda()
+    xc, xsc = xq[t].cpu().numpy(), xs[t].cpu().numpy()
+    y64, step = experts64(xc, xsc, wq.cpu().numpy(), ws.cpu().numpy(), np.arange(rows), offs)
+    assert_rounded(y, y64, step, torch.bfloat16)
 
 
 def test_experts_damaged_tables_stay_inside():
