@@ -244,14 +244,13 @@ void w8a8_resident_kernel(W8Args p)
 }
 
 // ---------------------------------------------------------------- tiles
-// One workgroup of 2 x 2 waves per BM tokens x BN channels, K in steps of 128
-// bytes.  Both tiles move to LDS with LDS-direct 16-byte loads into two stages
-// (rows of 128 bytes; the 16-byte chunk c of row r lies at c ^ (r / 2 % 8), so
-// that the rows one LDS cycle serves lie in different banks), and from there to
-// registers one K step ahead of the matrix instructions that use them.
+// One workgroup per BM tokens x BN channels, K in steps of BK bytes.  Both tiles
+// move to LDS with LDS-direct 16-byte loads into a ring of NST stages, and from
+// there to registers one K step ahead of the matrix instructions that use them.
+// Rows of a stage are BK bytes; the 16-byte chunk c of row r lies at c ^ (r /
+// SAME % C16), so that the 16 rows which LDS serves together lie in different
+// banks.
 typedef int i16v __attribute__((ext_vector_type(16)));
-constexpr int kTileWaves = 4;
-constexpr int kTileK = 128;
 
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, uint32_t lane_off, int k, uint8_t *lds)
 {
@@ -320,31 +319,32 @@ __device__ __forceinline__ bool expert_tile(const W8Args &p, W8Tile &t)
 // DENSE, SPLIT: K over workgroups, int32 partial sums out; EXPERTS: rows by expert
 enum W8Mode { DENSE, SPLIT, EXPERTS };
 
-// LDS stages of a tile size: as deep as it takes to cover the latency of the
-// loads with few workgroups on a CU
-template <int BM, int BN> constexpr int kStages = BM * BN <= 64 * 64 ? 4 : 2;
-
-template <int BM, int BN, W8Mode MODE>
-__global__ __launch_bounds__(kTileWaves * 64, 1)
+template <int BM, int BN, int NW, W8Mode MODE>
+__global__ __launch_bounds__(NW * 64, 1)
 void w8a8_tile_kernel(W8Args p)
 {
-    constexpr int NST = kStages<BM, BN>;
-    // 64 x 64: each wave has the whole tile and a quarter of every 128 bytes of K, so that no operand is read
-    // from LDS twice; otherwise each has a quarter of the tile.
+    constexpr int NST = BM * BN == 64 * 64 ? 4 : 2;   // LDS stages
+    constexpr int BK = 32 * NW;                       // bytes of K in one
+    // 64 x 64: each wave has the whole tile and 32 bytes of every stage's K, so that no operand is read from LDS
+    // twice; otherwise each has a quarter of the tile.
     constexpr bool KW = BM * BN == 64 * 64;
+    static_assert(KW || NW == 4, "2 x 2 waves share a tile");
     constexpr int NK = KW ? 1 : 4;                    // 32-byte pieces of a step that a wave multiplies
     constexpr int TC = KW ? 2 : BN / 64, TT = KW ? 2 : BM / 64;   // 32-wide blocks of a wave: channels, tokens
-    constexpr int LX = BM / 8 / kTileWaves, LW = BN / 8 / kTileWaves;   // LDS-direct loads of a wave per stage
-    constexpr int STAGE = (BM + BN) * kTileK;
+    constexpr int C16 = BK / 16, RPL = 64 / C16;      // 16-byte chunks of a row, rows of one LDS-direct load
+    constexpr int LX = BM / RPL / NW, LW = BN / RPL / NW;   // such loads of a wave per stage
+    constexpr int STAGE = (BM + BN) * BK;
+    constexpr int SAME = 256 / BK;                    // rows in 256 bytes: all of LDS's banks
+    static_assert(RPL * NW / SAME % C16 == 0, "every load stores its chunks in the same order");
     __shared__ __attribute__((aligned(1024))) uint8_t stages[NST * STAGE];
-    constexpr int THREADS = kTileWaves * 64, NS = (BM + 2 * BN + THREADS - 1) / THREADS;
+    constexpr int THREADS = NW * 64, NS = (BM + 2 * BN + THREADS - 1) / THREADS;
     __shared__ __attribute__((aligned(16))) float sc[NS * THREADS];   // token scales, channel scales, biases
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = KW ? 0 : wave & 1, wc = KW ? 0 : wave >> 1;
     W8Tile t;
-    int s0 = 0, s1 = (p.K + 2 * kTileK - 1) / (2 * kTileK) * 2, split = 0;   // steps, in pairs
+    int s0 = 0, s1 = (p.K + 2 * BK - 1) / (2 * BK) * 2, split = 0;   // steps, in pairs
     if constexpr (MODE == EXPERTS) {
         if (!expert_tile<BM, BN>(p, t)) return;
     } else {
@@ -376,15 +376,15 @@ void w8a8_tile_kernel(W8Args p)
     const auto xrs = buffer_rsrc(xb, (uint32_t)min(x_bytes, (int64_t)UINT32_MAX));
     const auto wrs = buffer_rsrc(wb, (uint32_t)((int64_t)n_valid * p.K));
 
-    // load i of the wave fills LDS rows 8 (4 i + wave) .. + 7, lane -> (row, stored chunk)
-    const int chunk0 = (lane & 7) ^ (((lane >> 4) + 4 * wave) & 7);
+    // load i of the wave fills LDS rows RPL (NW i + wave) .. + RPL - 1, lane -> (row, stored chunk)
+    const int chunk0 = (lane & (C16 - 1)) ^ ((RPL * wave + lane / C16) / SAME & (C16 - 1));
     auto place = [&](uint8_t *buf, int i) __attribute__((always_inline)) {
-        return buf + (i < LX ? 0 : BM * kTileK) + (kTileWaves * (i < LX ? i : i - LX) + wave) * 1024;
+        return buf + (i < LX ? 0 : BM * BK) + (NW * (i < LX ? i : i - LX) + wave) * 1024;
     };
     uint32_t off[LX + LW];
 #pragma unroll
     for (int i = 0; i < LX + LW; ++i) {
-        const int row = 8 * (kTileWaves * (i < LX ? i : i - LX) + wave) + (lane >> 3);
+        const int row = RPL * (NW * (i < LX ? i : i - LX) + wave) + lane / C16;
         int src = min(row, (i < LX ? m_valid : n_valid) - 1);
         if (MODE == EXPERTS && i < LX && p.row_slot) src = w8a8_source_row(p, t.first + src);
         off[i] = (uint32_t)src * (uint32_t)p.K + chunk0 * 16;
@@ -406,18 +406,18 @@ void w8a8_tile_kernel(W8Args p)
         }
 
     auto load_one = [&](int s, uint8_t *buf, int i) __attribute__((always_inline)) {
-        dma16(i < LX ? xrs : wrs, off[i], s * kTileK, place(buf, i));
+        dma16(i < LX ? xrs : wrs, off[i], s * BK, place(buf, i));
     };
-    const int full = p.K / kTileK;
+    const int full = p.K / BK;
     // the step that K ends inside, or an empty one that makes up a pair: bytes past K are zeros
     auto load_tail = [&](int s, uint8_t *buf) __attribute__((always_inline)) {
-        const int k = s * kTileK + chunk0 * 16;
+        const int k = s * BK + chunk0 * 16;
 #pragma unroll
         for (int j = 0; j < LX + LW; j += 4) {
             i4 v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = s * kTileK < p.K ? row16((j + i < LX ? xb : wb) + (off[j + i] - chunk0 * 16), k, p.K)
+                v[i] = s * BK < p.K ? row16((j + i < LX ? xb : wb) + (off[j + i] - chunk0 * 16), k, p.K)
                                         : i4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < 4; ++i) *reinterpret_cast<i4 *>(place(buf, j + i) + lane * 16) = v[i];
@@ -440,16 +440,16 @@ void w8a8_tile_kernel(W8Args p)
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // operand addresses: 32-row block, K chunk 2 k + lane / 32
+    // operand addresses: row lane % 32 of a block, K chunk 2 k + lane / 32
     int at[NK];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
-        at[k] = (lane & 31) * kTileK + ((2 * (KW ? wave : k) + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16;
+        at[k] = (lane & 31) * BK + ((2 * (KW ? wave : k) + (lane >> 5)) ^ ((lane & 31) / SAME & (C16 - 1))) * 16;
     auto token = [&](const uint8_t *buf, int b, int k) __attribute__((always_inline)) {
-        return *reinterpret_cast<const i4 *>(buf + (wt * TT + b) * 32 * kTileK + at[k]);
+        return *reinterpret_cast<const i4 *>(buf + (wt * TT + b) * 32 * BK + at[k]);
     };
     auto channel = [&](const uint8_t *buf, int b, int k) __attribute__((always_inline)) {
-        return *reinterpret_cast<const i4 *>(buf + BM * kTileK + (wc * TC + b) * 32 * kTileK + at[k]);
+        return *reinterpret_cast<const i4 *>(buf + BM * BK + (wc * TC + b) * 32 * BK + at[k]);
     };
 
     i16v acc[TC][TT];
@@ -574,7 +574,7 @@ void w8a8_tile_kernel(W8Args p)
     // in a loop: unrolled, this code is so long that fetching it takes longer than running it.
     constexpr int CW = KW ? BN : BN / 2, CHUNKS = CW / 4;   // channels of a wave, their chunks in a row
     constexpr int REGION = 32 * CW * 4;
-    static_assert(kTileWaves * REGION * (KW ? TT : 1) <= NST * STAGE, "the waves' rows fit");
+    static_assert(NW * REGION * (KW ? TT : 1) <= NST * STAGE, "the waves' rows fit");
     const int c8 = lane % (CW / 8) * 8, n = wc * CW + c8;
     f4 ws[2], bs[2];
     if constexpr (MODE != SPLIT)
@@ -603,54 +603,72 @@ void w8a8_tile_kernel(W8Args p)
         if constexpr (MODE == SPLIT) {
             int32_t *to = p.part + (int64_t)split * p.rows * p.N + o;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (wide) {
-                    if (n + 4 * h < n_valid) *reinterpret_cast<i4 *>(to + 4 * h) = v[h];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (n + 4 * h + i < n_valid) to[4 * h + i] = v[h][i];
-                }
-            }
+            for (int h = 0; h < 2; ++h)
+                if (n + 4 * h < n_valid) *reinterpret_cast<i4 *>(to + 4 * h) = v[h];
         } else {
             const float xs = sc[tok];
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = (float)v[i / 4][i % 4] * xs * ws[i / 4][i % 4] + bs[i / 4][i % 4];
-            if (wide) {
-                if (n < n_valid) put8(p.y, o, f, p.y_bf16);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (n + i < n_valid) put(p.y, o + i, f[i], p.y_bf16);
-            }
+            if (n < n_valid) put8(p.y, o, f, p.y_bf16);
         }
     };
+    // rows that start anywhere: value by value, neighbouring lanes neighbouring channels (623 x 23755 of K = 280
+    // in 30 us; 38 with a lane's eight in turn)
+    auto fetch1 = [&](const uint8_t *region, int r, int c) __attribute__((always_inline)) {
+        return *reinterpret_cast<const int *>(region + r * (CW * 4) + ((c / 4 ^ (r & (CHUNKS - 1))) * 16) + c % 4 * 4);
+    };
+    auto emit1 = [&](int tok, int c, int v) __attribute__((always_inline)) {
+        if (tok >= m_valid || c >= n_valid) return;
+        const int64_t o = (int64_t)(t.first + tok) * p.N + t.n0 + c;
+        if constexpr (MODE == SPLIT)
+            p.part[(int64_t)split * p.rows * p.N + o] = v;
+        else
+            put(p.y, o, (float)v * sc[tok] * sc[BM + c] + sc[BM + BN + c], p.y_bf16);
+    };
     if constexpr (KW) {
-        // every wave's sums of the tile; each then adds up and finishes 8 of a block's 32 rows
+        // every wave's sums of the tile; then eight lanes add up and finish a row
 #pragma unroll
         for (int b = 0; b < TT; ++b) stash(b, stages + (wave * TT + b) * REGION);
         sync(std::integral_constant<int, 0>{});
+        if (wide) {
 #pragma unroll
-        for (int b = 0; b < TT; ++b) {
-            const int r = wave * 8 + lane / 8;
-            i4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+            for (int row = tid / 8; row < BM; row += THREADS / 8) {
+                i4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-            for (int q = 0; q < kTileWaves; ++q)
+                for (int q = 0; q < NW; ++q)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) v[h] += fetch(stages + (q * TT + b) * REGION, r, h);
-            emit(b * 32 + r, v);
+                    for (int h = 0; h < 2; ++h) v[h] += fetch(stages + (q * TT + row / 32) * REGION, row % 32, h);
+                emit(row, v);
+            }
+        } else {
+#pragma unroll 2
+            for (int row = wave; row < BM; row += NW) {
+                int v = 0;
+#pragma unroll
+                for (int q = 0; q < NW; ++q) v += fetch1(stages + (q * TT + row / 32) * REGION, row % 32, lane);
+                emit1(row, lane, v);
+            }
         }
     } else {
         uint8_t *mine = stages + wave * REGION;
         constexpr int RSTEP = 64 / (CW / 8);
 #pragma unroll
         for (int b = 0; b < TT; ++b) {
+            const int tok0 = (wt * TT + b) * 32;
             stash(b, mine);
+            if (wide) {
 #pragma unroll 4
-            for (int r = lane / (CW / 8); r < 32; r += RSTEP) {
-                const i4 v[2] = {fetch(mine, r, 0), fetch(mine, r, 1)};
-                emit((wt * TT + b) * 32 + r, v);
+                for (int r = lane / (CW / 8); r < 32; r += RSTEP) {
+                    const i4 v[2] = {fetch(mine, r, 0), fetch(mine, r, 1)};
+                    emit(tok0 + r, v);
+                }
+            } else {
+#pragma unroll 4
+                for (int i = 0; i < 32 * CW / 64; ++i) {
+                    const int r = i / (CW / 64), c = i % (CW / 64) * 64 + lane;
+                    emit1(tok0 + r, wc * CW + c, fetch1(mine, r, c));
+                }
             }
         }
     }
@@ -716,21 +734,25 @@ void stream(const W8Args &a, hipStream_t s)
         stream_launch<2, true, GROUPED>(a, s);
 }
 
-template <int B, W8Mode MODE>
+constexpr int kCUs = 256;
+
+template <int B, int NW, W8Mode MODE>
 void tile_launch(const W8Args &a, int64_t tiles, hipStream_t s)
 {
-    w8a8_tile_kernel<B, B, MODE><<<(unsigned)round_up(tiles, 8), kTileWaves * 64, 0, s>>>(a);
+    w8a8_tile_kernel<B, B, NW, MODE><<<(unsigned)round_up(tiles, 8), NW * 64, 0, s>>>(a);
 }
 
 template <W8Mode MODE>
 void tile_launch(const W8Args &a, int size, int64_t tiles, hipStream_t s)
 {
-    if (size == 64)
-        tile_launch<64, MODE>(a, tiles, s);
+    if (size == 64 && tiles <= kCUs)
+        tile_launch<64, 8, MODE>(a, tiles, s);
+    else if (size == 64)
+        tile_launch<64, 4, MODE>(a, tiles, s);
     else if (size == 128)
-        tile_launch<128, MODE>(a, tiles, s);
+        tile_launch<128, 4, MODE>(a, tiles, s);
     else
-        tile_launch<256, MODE>(a, tiles, s);
+        tile_launch<256, 4, MODE>(a, tiles, s);
 }
 
 // Rows up to which a dense product streams the weights: one pass serves 16.
@@ -742,7 +764,7 @@ struct W8Plan {
 };
 
 // workgroups of one launch: a grid holds fewer than 2^32 threads
-constexpr int64_t kMaxTiles = (int64_t)1 << 24;
+constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 
 // The tile size and split with the least estimated time: a start and an end,
 // then per 128 bytes of K a time for each tile a CU has to take (one tile of
@@ -753,16 +775,16 @@ W8Plan w8_plan(int rows, int N, int K)
         int size;
         double ends, step, least;                     // microseconds
     };
-    constexpr Cost kCosts[] = {{64, 4.0, 0.25, 0.2}, {128, 6.0, 0.56, 0.56}, {256, 14.0, 1.6, 1.6}};
-    const int pairs = (K + 2 * kTileK - 1) / (2 * kTileK);
+    constexpr Cost kCosts[] = {{64, 5.5, 0.25, 0.15}, {128, 6.0, 0.56, 0.56}, {256, 14.0, 1.6, 1.6}};
+    const int pairs = (K + 255) / 256;
     W8Plan best = {64, 1, 0};
     double time = -1.0;
     for (const Cost &c : kCosts) {
         const int64_t tiles = (((int64_t)rows + c.size - 1) / c.size) * (((int64_t)N + c.size - 1) / c.size);
         if (tiles >= kMaxTiles && c.size < 256) continue;
-        for (int splits = 1; splits <= 8 && (splits == 1 || splits <= pairs); splits *= 2) {
-            const int64_t each = (tiles * splits + 255) / 256;
-            const double step = each * c.step > c.least ? each * c.step : c.least;
+        for (int splits = 1; splits <= 8 && (splits == 1 || splits * 2 <= pairs); splits *= 2) {
+            const int64_t each = (tiles * splits + kCUs - 1) / kCUs;
+            const double step = each > 1 ? each * c.step : c.least;
             const double reduce = splits > 1 ? 3.0 + (double)splits * rows * N * 8 / 4e6 : 0.0;
             const double us = c.ends + (pairs + splits - 1) / splits * 2 * step + reduce;
             if (time < 0.0 || us < time) {
@@ -788,8 +810,8 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
     W8Args a = args;
     if (a.rows <= kStreamRows) {
         const int units = a.K / 128;
-        if (a.rows >= 4 && a.N >= 3 * 256 * 16 && units > 2 * W && units <= 4 * W)
-            w8a8_resident_kernel<4><<<256, W * 64, 0, s>>>(a);
+        if (a.rows >= 4 && a.N >= 3 * kCUs * 16 && units > 2 * W && units <= 4 * W)
+            w8a8_resident_kernel<4><<<kCUs, W * 64, 0, s>>>(a);
         else
             stream<false>(a, s);
         return hipGetLastError();

@@ -451,9 +451,13 @@ hipError_t launch_moe_unpermute_backward(const void *dy, const void *yp, int bf1
     };
     auto pick = [&](auto b, auto item) {
         constexpr bool B = decltype(b)::value;
-        if (items <= 64)                              // one wave has the whole row
+        // as many waves as have a piece of the row, up to four
+        if (items <= 64)
             return far ? launch(moe_unpermute_backward_kernel<true, B, 1>, 1, item)
                        : launch(moe_unpermute_backward_kernel<false, B, 1>, 1, item);
+        if (items <= 128)
+            return far ? launch(moe_unpermute_backward_kernel<true, B, 2>, 2, item)
+                       : launch(moe_unpermute_backward_kernel<false, B, 2>, 2, item);
         return far ? launch(moe_unpermute_backward_kernel<true, B, 4>, 4, item)
                    : launch(moe_unpermute_backward_kernel<false, B, 4>, 4, item);
     };
