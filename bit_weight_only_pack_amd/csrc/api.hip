@@ -2,6 +2,7 @@
 // dispatch to the launchers.  Nothing here allocates device memory; every
 // error is detected before the first enqueue.
 #include "lowbit_internal.hpp"
+#include "w8a8_sort.hpp"
 
 #include <vector>
 

@@ -16,7 +16,7 @@
 // the B operand: a lane then holds four consecutive channels of one token.
 #include <type_traits>
 
-#include "lowbit_internal.hpp"
+#include "w8a8_sort.hpp"
 
 namespace lowbit {
 

@@ -13,7 +13,7 @@
 // fixed order of summation, in fp32.
 #include <type_traits>
 
-#include "lowbit_internal.hpp"
+#include "w8a8_sort.hpp"
 
 namespace lowbit {
 

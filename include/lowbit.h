@@ -303,7 +303,9 @@ int lowbit_gemm_w8a8(int M, int N, int K, const int8_t *xq, const float *x_scale
                      const float *w_scale, const float *bias, void *y, int y_dtype,
                      void *workspace, size_t ws_bytes, void *stream);
 
-/* Workspace bytes of lowbit_gemm_w8a8 (0 if none is needed or the shape is invalid). */
+/* Workspace bytes of lowbit_gemm_w8a8 (0 if none is needed or the shape is
+ * invalid).  Fewer rows can need more (K is split where the tiles are few): a
+ * buffer kept for several shapes takes the largest of their figures. */
 size_t lowbit_gemm_w8a8_workspace_bytes(int M, int N, int K);
 
 /*

@@ -68,8 +68,8 @@ def _case(T, top_k, E, El, seed=0):
     return rng, rs, sr, int(of[-1])
 
 
-@pytest.mark.parametrize("T,top_k,E,El", [(1, 1, 1, 1), (1, 8, 16, 16), (33, 3, 8, 3), (700, 2, 8, 8)])
-@pytest.mark.parametrize("row_bytes", [8, 16, 24, 264, 2048, 4096, 6160, 40960])
+@pytest.mark.parametrize("T,top_k,E,El", [(1, 1, 1, 1), (1, 8, 16, 16), (33, 3, 8, 3), (700, 2, 8, 8), (40, 17, 40, 33)])
+@pytest.mark.parametrize("row_bytes", [0, 8, 16, 24, 264, 2048, 4096, 6160, 40960])
 def test_permute_bytes(T, top_k, E, El, row_bytes):
     rng, rs, sr, n = _case(T, top_k, E, El, row_bytes)
     x = rng.integers(0, 256, (T, row_bytes)).astype(np.uint8)

@@ -295,6 +295,14 @@ def test_experts_gather_past_2_31(x_rows, rows):
     assert_rounded(y, y64, step, torch.bfloat16)
 
 
+@pytest.mark.parametrize("rows", [6, 90])
+def test_experts_k_zero(rows):
+    y = run_experts(torch.empty((rows, 0), dtype=torch.int8, device="cuda"), dev(np.ones(rows, np.float32)),
+                    torch.empty((3, 20, 0), dtype=torch.int8, device="cuda"),
+                    dev(np.ones((3, 20), np.float32)), None, 1, dev(np.array([0, 2, 2, rows], np.int32)), rows, "f16")
+    assert bool((y == 0).all())
+
+
 def test_experts_damaged_tables_stay_inside():
     """Slots and offsets outside their ranges read and write inside the matrices (what they compute is undefined)."""
     rng = np.random.default_rng(2)
