@@ -59,199 +59,6 @@ __device__ __forceinline__ i4 row16(const int8_t *row, int k, int K)
     return i4{lo.x & lm, lo.y & lm, hi.x & hm, hi.y & hm};
 }
 
-// ---------------------------------------------------------------- streaming
-// Few rows: the weights' stream is the cost.  A workgroup takes a run of 16
-// channels for 16 rows at a time; its 8 waves share K out in units of 128 bytes
-// (unit u of wave w is 8 u + w, so the waves together read whole spans of each
-// row) and add their int32 sums through LDS.  Weights go straight to registers.
-// Where U units are all of a wave's K, every load is under way at once; LOOP:
-// the next U are loaded while U are multiplied.  Rows past the last (of the
-// activation or the weight) are read as copies of the last one and not stored.
-constexpr int W = 8;                                  // waves
-
-template <int U, bool LOOP, bool GROUPED>
-__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4)))
-void w8a8_stream_kernel(W8Args p)
-{
-    __shared__ __attribute__((aligned(16))) int part[W][256];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r16 = lane & 15, kq = lane >> 4;
-    const int n0 = blockIdx.x * 16;
-    int first = 0, last = p.rows;
-    const int8_t *w = p.w;
-    const float *ws = p.ws;
-    if constexpr (GROUPED) {
-        const int e = blockIdx.y;
-        first = max(p.offsets[e], 0);
-        last = min(p.offsets[e + 1], p.rows);
-        if (first >= last) return;
-        w += (int64_t)e * p.N * p.K;
-        ws += (int64_t)e * p.N;
-    }
-    w += (int64_t)n0 * p.K;
-    const int units = p.K / 128;                      // whole ones
-    const int mine = units > wave ? (units - wave + W - 1) / W : 0;
-    const int nb = (mine + U - 1) / U;                // batches of this wave
-    const uint32_t row = (uint32_t)min(r16, p.N - 1 - n0) * (uint32_t)p.K + kq * 16;
-    const int tm = (tid >> 4) & 15, n = n0 + (tid & 15);   // the sum that this thread finishes
-    const float wscale = ws[min(n, p.N - 1)];
-
-    for (int m0 = first; m0 < last; m0 += 16) {
-        const int8_t *xr = p.x + (int64_t)w8a8_source_row(p, min(m0 + r16, last - 1)) * p.K + kq * 16;
-        const float xs = p.xs[w8a8_source_row(p, min(m0 + tm, last - 1))];
-        i4 wv[LOOP ? 2 : 1][U][2], xv[LOOP ? 2 : 1][U][2], acc = {0, 0, 0, 0};
-        auto load = [&](int b, i4 (&v)[U][2], i4 (&x)[U][2]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!LOOP && u >= mine) continue;
-                const int k = ((LOOP ? min(b * U + u, mine - 1) : u) * W + wave) * 128;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[u][h] = __builtin_nontemporal_load(reinterpret_cast<const i4a *>(w + k + 64 * h + row));
-                    x[u][h] = *reinterpret_cast<const i4a *>(xr + k + 64 * h);
-                }
-            }
-        };
-        auto multiply = [&](int b, const i4 (&v)[U][2], const i4 (&x)[U][2]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (b * U + u < mine)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[u][h], x[u][h], acc, 0, 0, 0);
-        };
-        // K behind the whole units: 64 bytes of a wave
-        const int k0 = units * 128 + wave * 64;
-        i4 xt, wt;
-        auto load_tail = [&]() __attribute__((always_inline)) {
-            if (k0 >= p.K) return;
-            xt = row16(xr - kq * 16, k0 + kq * 16, p.K);
-            wt = row16(w + row - kq * 16, k0 + kq * 16, p.K);
-        };
-        if constexpr (!LOOP) {
-            load(0, wv[0], xv[0]);
-            load_tail();
-            multiply(0, wv[0], xv[0]);
-        } else if (nb > 0) {
-            load(0, wv[0], xv[0]);
-            int b = 0;
-            for (; b + 2 < nb; b += 2) {
-                load(b + 1, wv[1], xv[1]);
-                multiply(b, wv[0], xv[0]);
-                load(b + 2, wv[0], xv[0]);
-                multiply(b + 1, wv[1], xv[1]);
-            }
-            if (b + 1 < nb) {
-                load(b + 1, wv[1], xv[1]);
-                multiply(b, wv[0], xv[0]);
-                multiply(b + 1, wv[1], xv[1]);
-            } else {
-                multiply(b, wv[0], xv[0]);
-            }
-        }
-        if (LOOP) load_tail();
-        if (k0 < p.K) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wt, xt, acc, 0, 0, 0);
-        // lane: token r16, channels 4 kq .. 4 kq + 3
-        *reinterpret_cast<i4 *>(&part[wave][r16 * 16 + kq * 4]) = acc;
-        __syncthreads();
-        if (tid < 256) {
-            int sum = 0;
-#pragma unroll
-            for (int q = 0; q < W; ++q) sum += part[q][tid];
-            if (m0 + tm < last && n < p.N) {
-                float v = (float)sum * xs * wscale;
-                if (p.bias) v += p.bias[n];
-                put(p.y, (int64_t)(m0 + tm) * p.N + n, v, p.y_bf16);
-            }
-        }
-        if (m0 + 16 < last) __syncthreads();          // the sums are read before the next rows' are written
-    }
-}
-
-// The same for many channels and several rows (dense): one workgroup per CU
-// goes through runs of 16 channels, the rows' operands staying in registers
-// and the next run's weights on their way while a run is finished.
-template <int U>
-__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(2)))
-void w8a8_resident_kernel(W8Args p)
-{
-    __shared__ __attribute__((aligned(16))) int part[2][W][256];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r16 = lane & 15, kq = lane >> 4;
-    const int runs = (p.N + 15) / 16, step = gridDim.x;
-    const int units = p.K / 128;
-    const int mine = units > wave ? (units - wave + W - 1) / W : 0;
-    const int tm = (tid >> 4) & 15, tn = tid & 15;    // the sum that this thread finishes
-    const int8_t *xr = p.x + (int64_t)min(r16, p.rows - 1) * p.K + kq * 16;
-    const float xs = p.xs[min(tm, p.rows - 1)];
-    const int k0 = units * 128 + wave * 64;           // K behind the whole units: 64 bytes of a wave
-    const i4 xt = k0 < p.K ? row16(xr - kq * 16, k0 + kq * 16, p.K) : i4{0, 0, 0, 0};
-    i4 xv[U][2], wv[2][U][2], wt[2];
-    float wscale[2];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            xv[u][h] = *reinterpret_cast<const i4a *>(xr + (max(min(u, mine - 1), 0) * W + wave) * 128 + 64 * h);
-    auto load = [&](int run, int to) __attribute__((always_inline)) {
-        const int r = min(run, runs - 1);
-        const int8_t *w = p.w + (int64_t)r * 16 * p.K;
-        const uint32_t row = (uint32_t)min(r16, p.N - 1 - r * 16) * (uint32_t)p.K + kq * 16;
-        wscale[to] = p.ws[min(r * 16 + tn, p.N - 1)];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                wv[to][u][h] = __builtin_nontemporal_load(reinterpret_cast<const i4a *>(
-                    w + (max(min(u, mine - 1), 0) * W + wave) * 128 + 64 * h + row));
-        if (k0 < p.K) wt[to] = row16(w + row - kq * 16, k0 + kq * 16, p.K);
-    };
-    auto finish = [&](int run, int from) __attribute__((always_inline)) {
-        i4 acc = {0, 0, 0, 0};
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (u < mine)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[from][u][h], xv[u][h], acc, 0, 0, 0);
-        if (k0 < p.K) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wt[from], xt, acc, 0, 0, 0);
-        *reinterpret_cast<i4 *>(&part[from][wave][r16 * 16 + kq * 4]) = acc;
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay under way
-        if (tid < 256) {
-            int s = 0;
-#pragma unroll
-            for (int q = 0; q < W; ++q) s += part[from][q][tid];
-            const int n = run * 16 + tn;
-            if (tm < p.rows && n < p.N) {
-                float v = (float)s * xs * wscale[from];
-                if (p.bias) v += p.bias[n];
-                put(p.y, (int64_t)tm * p.N + n, v, p.y_bf16);
-            }
-        }
-        // the two halves of `part` take turns: a half is written again only behind the other's barrier,
-        // which every wave passes after it has read the first
-    };
-    load(blockIdx.x, 0);
-    for (int run = blockIdx.x; run < runs; run += 2 * step) {
-        load(run + step, 1);
-        finish(run, 0);
-        if (run + step >= runs) break;
-        load(run + 2 * step, 0);
-        finish(run + step, 1);
-    }
-}
-
-// ---------------------------------------------------------------- tiles
-// One workgroup per BM tokens x BN channels, K in steps of BK bytes.  Both tiles
-// move to LDS with LDS-direct 16-byte loads into a ring of NST stages, and from
-// there to registers one K step ahead of the matrix instructions that use them.
-// Rows of a stage are BK bytes; the 16-byte chunk c of row r lies at c ^ (r /
-// SAME % C16), so that the 16 rows which LDS serves together lie in different
-// banks.
-typedef int i16v __attribute__((ext_vector_type(16)));
-
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, uint32_t lane_off, int k, uint8_t *lds)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)lds, 16, lane_off, k, 0, 0);
@@ -264,6 +71,199 @@ __device__ __forceinline__ void wait_vm()
     static_assert(N >= 0 && N < 64, "vmcnt range");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
+
+// ---------------------------------------------------------------- streaming
+// Few rows: the weights' stream is the cost.  A workgroup takes CH channels and
+// up to 8 XL rows; its WV waves share K out in units of 128 bytes (wave w has
+// units WV u + w, so the waves together read whole spans of each row).  Every
+// wave runs a ring of its own in LDS: LDS-direct loads bring a unit of the rows
+// and of the channels NST units ahead, and the wave that loaded it is the one
+// that reads it, so it waits for its own load counter and there is no barrier.
+// Reading the next units through LDS instead of registers keeps 1 KB of each
+// load in one piece and leaves the registers to the sums.  The int32 sums of the
+// waves are added through LDS at the end.  Rows past the last, of the activation
+// or the weight, are read as copies of the last one and not stored.
+//
+// Bound: the weights' bytes once (and some 2 us of start and end).  Measured
+// (us, weights not in the caches), CH / WV / NST by column, and tiles of 64:
+//                          16/8/3   32/8/2   64/4/2   tiles
+//   1024 x 4096   1 row      2.8      3.7      4.6      8.1
+//   4096 x 4096   1 row      4.5      4.9      5.7      9.1
+//                16 rows     4.8      5.2      6.3      9.6
+//                32 rows     5.6      6.1      7.9      8.5
+//                64 rows     7.2*     8.0*    10.8      9.3     (* 16/8/2, 32/4/2)
+//   6144 x 4096  16 rows     7.6      6.4      6.8      8.5
+//                64 rows    11.5*     8.9*    11.2      9.5
+//  14336 x 4096  16 rows    15.1     12.5     10.6     12.2
+//                32 rows    16.9     13.8     11.9     12.4
+//  28672 x 4096  16 rows    30.5     27.6     23.6     26.9     (117 MB: 5.0 TB/s)
+//                32 rows    36.3     31.6     28.8     27.5
+template <int CH, int WV, int NST, int XL>
+constexpr int kRingBytes = WV * NST * (8 * XL + CH) * 128;
+
+// rows `first` .. `last` - 1 of the output, at most 8 XL of them, channels n0 ..
+template <int CH, int WV, int NST, int XL>
+__device__ __forceinline__ void w8a8_stream_rows(const W8Args &p, uint8_t *ring, const int8_t *wb, const float *ws,
+                                                 int first, int last, int n0)
+{
+    constexpr int NB = CH / 16, TB = XL > 1 ? XL / 2 : 1;      // blocks of 16 channels, of 16 tokens
+    constexpr int L = XL + CH / 8, STAGE = (8 * XL + CH) * 128;   // loads of a unit, its bytes
+    constexpr int THREADS = WV * 64, SUMS = (16 * TB * CH + THREADS - 1) / THREADS;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, kq = lane >> 4;
+    const int n_valid = min(CH, p.N - n0), m_valid = last - first;
+    const int units = p.K / 128;                      // whole ones
+    const int mine = units > wave ? (units - wave + WV - 1) / WV : 0;
+
+    // what the sums that this thread finishes are multiplied with
+    const int n = tid % CH;
+    const float wscale = ws[min(n, n_valid - 1)], bias = p.bias ? p.bias[n0 + min(n, n_valid - 1)] : 0.f;
+    float xs[SUMS];
+#pragma unroll
+    for (int j = 0; j < SUMS; ++j)
+        xs[j] = p.xs[w8a8_source_row(p, first + min((j * THREADS + tid) / CH, m_valid - 1))];
+    // K behind the whole units: 64 bytes of the first waves
+    const int k0 = units * 128 + wave * 64;
+    i4 xt[TB], wt[NB];
+    if (k0 < p.K) {
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+            xt[b] = row16(p.x + (int64_t)w8a8_source_row(p, first + min(b * 16 + r16, m_valid - 1)) * p.K, k0 + kq * 16, p.K);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            wt[b] = row16(wb + (int64_t)min(b * 16 + r16, n_valid - 1) * p.K, k0 + kq * 16, p.K);
+    }
+
+    // a load fills 8 rows of 128 bytes; chunk c of row r lies at c ^ (r / 2 % 8), so that the 16 rows which LDS
+    // serves together lie in different banks
+    const auto wrs = buffer_rsrc(wb, (uint32_t)((int64_t)n_valid * p.K));
+    const int8_t *xp[XL];
+    uint32_t off[CH / 8];
+    const int put_chunk = ((lane & 7) ^ (lane >> 4)) * 16;
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+        xp[i] = p.x + (int64_t)w8a8_source_row(p, first + min(8 * i + (lane >> 3), m_valid - 1)) * p.K +
+                (put_chunk ^ (i & 1) * 64);
+#pragma unroll
+    for (int i = 0; i < CH / 8; ++i)
+        off[i] = (uint32_t)min(8 * i + (lane >> 3), n_valid - 1) * (uint32_t)p.K + (put_chunk ^ (i & 1) * 64);
+    uint8_t *own = ring + wave * NST * STAGE;
+    auto issue = [&](int u, int slot) __attribute__((always_inline)) {
+        const int k = (u * WV + wave) * 128;
+        uint8_t *to = own + slot * STAGE;
+#pragma unroll
+        for (int i = 0; i < XL; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xp[i] + k),
+                                             (__attribute__((address_space(3))) void *)(to + i * 1024), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < CH / 8; ++i) dma16(wrs, off[i], k, to + (XL + i) * 1024);
+    };
+    i4 acc[TB][NB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[t][b] = i4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < NST; ++u)
+        if (u < mine) issue(u, u);
+
+    int slot = 0;
+    for (int u = 0; u < mine; ++u) {
+        // unit u has landed: where NST - 1 more are under way their loads may stay so, else all are waited for
+        __builtin_amdgcn_sched_barrier(0);
+        if (u + NST <= mine)
+            wait_vm<(NST - 1) * L>();
+        else
+            wait_vm<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t *st = own + slot * STAGE;
+        i4 x[TB][2], w[NB][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = ((4 * h + kq) ^ (r16 >> 1)) * 16;
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+                x[t][h] = XL == 1 ? *reinterpret_cast<const i4 *>(st + (r16 & 7) * 128 + ((4 * h + kq) ^ ((r16 & 7) >> 1)) * 16)
+                                  : *reinterpret_cast<const i4 *>(st + (t * 16 + r16) * 128 + at);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                w[b][h] = *reinterpret_cast<const i4 *>(st + XL * 1024 + (b * 16 + r16) * 128 + at);
+        }
+        // in registers: the slot is free
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (u + NST < mine) issue(u + NST, slot);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    acc[t][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[b][h], x[t][h], acc[t][b], 0, 0, 0);
+        slot = slot + 1 == NST ? 0 : slot + 1;
+    }
+    if (k0 < p.K)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                acc[t][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wt[b], xt[t], acc[t][b], 0, 0, 0);
+
+    __syncthreads();                                  // every ring is done with
+    int *part = reinterpret_cast<int *>(ring);        // [waves][16 TB][CH]
+    static_assert(WV * 16 * TB * CH * 4 <= kRingBytes<CH, WV, NST, XL>, "the sums fit the rings");
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)                  // lane: token r16, channels 4 kq .. 4 kq + 3
+            *reinterpret_cast<i4 *>(part + ((wave * TB + t) * 16 + r16) * CH + b * 16 + kq * 4) = acc[t][b];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < SUMS; ++j) {
+        const int i = j * THREADS + tid, m = i / CH;
+        if (m >= m_valid || n >= n_valid) continue;
+        int s = 0;
+#pragma unroll
+        for (int q = 0; q < WV; ++q) s += part[q * 16 * TB * CH + i];
+        put(p.y, (int64_t)(first + m) * p.N + n0 + n, (float)s * xs[j] * wscale + bias, p.y_bf16);
+    }
+}
+
+template <int CH, int WV, int NST, int XL>
+__global__ __launch_bounds__(WV * 64) void w8a8_stream_kernel(W8Args p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[kRingBytes<CH, WV, NST, XL>];
+    const int n0 = blockIdx.x * CH;
+    w8a8_stream_rows<CH, WV, NST, XL>(p, ring, p.w + (int64_t)n0 * p.K, p.ws + n0, 0, p.rows, n0);
+}
+
+// By expert: 16 rows at a time, eight where there are no more
+template <int CH, int WV, int NST>
+__global__ __launch_bounds__(WV * 64) void w8a8_stream_experts_kernel(W8Args p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[kRingBytes<CH, WV, NST, 2>];
+    const int e = blockIdx.y, n0 = blockIdx.x * CH;
+    const int last = min(p.offsets[e + 1], p.rows);
+    const int64_t row = (int64_t)e * p.N + n0;
+    for (int m0 = max(p.offsets[e], 0); m0 < last; m0 += 16) {
+        if (last - m0 > 8)
+            w8a8_stream_rows<CH, WV, NST, 2>(p, ring, p.w + row * p.K, p.ws + row, m0, min(m0 + 16, last), n0);
+        else
+            w8a8_stream_rows<CH, WV, NST, 1>(p, ring, p.w + row * p.K, p.ws + row, m0, last, n0);
+        if (m0 + 16 < last) __syncthreads();          // the sums are read before the next rows' rings are filled
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+// One workgroup per BM tokens x BN channels, K in steps of BK bytes.  Both tiles
+// move to LDS with LDS-direct 16-byte loads into a ring of NST stages, and from
+// there to registers one K step ahead of the matrix instructions that use them.
+// Rows of a stage are BK bytes; the 16-byte chunk c of row r lies at c ^ (r /
+// SAME % C16), so that the 16 rows which LDS serves together lie in different
+// banks.
+typedef int i16v __attribute__((ext_vector_type(16)));
 
 // The tile of this workgroup among the tiles of all experts (their rows cut
 // into runs of BM): consecutive numbers go over an expert's row tiles first, so
@@ -714,27 +714,40 @@ void reduce_launch(const W8Args &a, hipStream_t s)
 
 namespace {
 
-template <int U, bool LOOP, bool GROUPED>
-void stream_launch(const W8Args &a, hipStream_t s)
+constexpr int kCUs = 256;
+
+// A dense product streams the weights where one pass over them serves all rows
+// faster than tiles do: up to 16 rows, and up to 64 where a wave of workgroups
+// takes at most 32 channels each (w8a8_stream_rows has the figures).
+bool w8_streams(int rows, int N)
 {
-    w8a8_stream_kernel<U, LOOP, GROUPED><<<dim3((a.N + 15) / 16, GROUPED ? a.E : 1), W * 64, 0, s>>>(a);
+    return rows <= 16 || (rows <= 64 && N <= 32 * kCUs);
 }
 
-template <bool GROUPED>
+template <int CH, int WV, int NST, int XL>
 void stream(const W8Args &a, hipStream_t s)
 {
-    const int units = a.K / 128;
-    if (units <= W)
-        stream_launch<1, false, GROUPED>(a, s);
-    else if (units <= 2 * W)
-        stream_launch<2, false, GROUPED>(a, s);
-    else if (units <= 4 * W)
-        stream_launch<4, false, GROUPED>(a, s);
-    else
-        stream_launch<2, true, GROUPED>(a, s);
+    w8a8_stream_kernel<CH, WV, NST, XL><<<(a.N + CH - 1) / CH, WV * 64, 0, s>>>(a);
 }
 
-constexpr int kCUs = 256;
+// As few channels a workgroup as give every CU one, as many rows as there are.
+template <int XL>
+void stream(const W8Args &a, hipStream_t s)
+{
+    constexpr bool kMany = XL == 8;                   // the rings of 64 rows leave room for less
+    if (a.N <= 16 * kCUs)
+        stream<16, 8, kMany ? 2 : 3, XL>(a, s);
+    else if (XL > 2 || a.N <= 32 * kCUs)
+        stream<32, kMany ? 4 : 8, 2, XL>(a, s);
+    else if constexpr (XL <= 2)
+        stream<64, 4, 2, XL>(a, s);
+}
+
+template <int CH, int WV, int NST>
+void stream_experts(const W8Args &a, hipStream_t s)
+{
+    w8a8_stream_experts_kernel<CH, WV, NST><<<dim3((a.N + CH - 1) / CH, a.E), WV * 64, 0, s>>>(a);
+}
 
 template <int B, int NW, W8Mode MODE>
 void tile_launch(const W8Args &a, int64_t tiles, hipStream_t s)
@@ -754,9 +767,6 @@ void tile_launch(const W8Args &a, int size, int64_t tiles, hipStream_t s)
     else
         tile_launch<256, 4, MODE>(a, tiles, s);
 }
-
-// Rows up to which a dense product streams the weights: one pass serves 16.
-constexpr int kStreamRows = 16;
 
 struct W8Plan {
     int size, splits;                                 // tile, workgroups that share K
@@ -800,7 +810,7 @@ W8Plan w8_plan(int rows, int N, int K)
 
 size_t gemm_w8a8_workspace(int M, int N, int K)
 {
-    if (M <= kStreamRows) return 0;
+    if (w8_streams(M, N)) return 0;
     const W8Plan pl = w8_plan(M, N, K);
     return pl.splits > 1 ? (size_t)pl.splits * M * N * sizeof(int32_t) : 0;
 }
@@ -808,12 +818,15 @@ size_t gemm_w8a8_workspace(int M, int N, int K)
 hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 {
     W8Args a = args;
-    if (a.rows <= kStreamRows) {
-        const int units = a.K / 128;
-        if (a.rows >= 4 && a.N >= 3 * kCUs * 16 && units > 2 * W && units <= 4 * W)
-            w8a8_resident_kernel<4><<<kCUs, W * 64, 0, s>>>(a);
+    if (w8_streams(a.rows, a.N)) {
+        if (a.rows <= 8)
+            stream<1>(a, s);
+        else if (a.rows <= 16)
+            stream<2>(a, s);
+        else if (a.rows <= 32)
+            stream<4>(a, s);
         else
-            stream<false>(a, s);
+            stream<8>(a, s);
         return hipGetLastError();
     }
     const W8Plan pl = w8_plan(a.rows, a.N, a.K);
@@ -828,18 +841,29 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
     return hipGetLastError();
 }
 
-// The kernel goes by the rows that an expert has on average.  Measured (us;
-// streaming / tiles of 64 / 128 / 256), 128 experts of 1536 x 2048 and 8 of
-// 4096 x 4096:
-//   rows an expert      4                   8                   64                 256
-//   128 experts   78 / 75 / 74 / 91   90 / 80 / 78 / 95   443 / 108 / 93 / 110   - / 257 / 176 / 182
-//   8 experts     28 / 32 / 41 / 57   31 / 32 / 39 / 55   152 /  39 / 40 /  55   - /  78 /  76 /  59
+// The kernel goes by the rows that an expert has on average, each with both
+// sides measured (us):
+//   rows an expert                            1        4        8       12       16
+//   128 experts of 1536 x 2048: stream       45       63       65       72       85
+//                               tiles of 64  56       76       79       82       84
+//   8 experts of 4096 x 4096:   stream       15       27       28       30       35
+//                               tiles of 64  17       32       32       32       32
+//   rows an expert                           64                 256
+//   128 experts: tiles of 64 / 128 / 256     108 /  93 / 110    257 / 176 / 182
+//   8 experts                                 39 /  40 /  55     78 /  76 /  59
+// A ring of four waves and three stages holds twelve units of K: with fewer of
+// them two waves and two stages serve more workgroups a CU (128 experts of
+// 2048 x 768, 1 / 4 / 8 rows each: 25 / 35 / 36 against 32 / 45 / 47; of
+// 1536 x 2048: 47 / 66 / 69 against 45 / 63 / 65).
 hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
 {
     // the rows' offsets inside x are 32-bit in the tile kernel when they are gathered
     const bool far = a.row_slot != nullptr && (int64_t)a.x_rows * a.K >= ((int64_t)1 << 32);
-    if (a.rows < 6 * a.E || far) {
-        stream<true>(a, s);
+    if (a.rows <= 12 * a.E || far) {
+        if (a.K < 12 * 128)
+            stream_experts<32, 2, 2>(a, s);
+        else
+            stream_experts<32, 4, 3>(a, s);
         return hipGetLastError();
     }
     int size = a.rows < 64 * a.E ? 64 : a.rows < 256 * a.E || a.K < 4096 ? 128 : 256;

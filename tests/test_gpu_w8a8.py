@@ -60,6 +60,12 @@ SHAPES = [
     # prefill
     (255, 511, 1024), (256, 256, 4096), (257, 513, 2056), (300, 1000, 384), (512, 6144, 256), (1030, 770, 1288),
     (2048, 2056, 520), (4097, 40, 144),
+    # weights streamed: every width of channels and rows, K below one unit of a wave, rings that are not full and full
+    (8, 4096, 1000), (9, 4097, 1160), (16, 4095, 7176), (17, 4090, 136), (32, 4000, 4104), (33, 4095, 2184),
+    (48, 4096, 64), (64, 4081, 6152), (1, 4100, 4104), (8, 8190, 264), (16, 8192, 2312), (18, 4120, 4088),
+    (32, 8177, 1032), (33, 4111, 72), (64, 8192, 520), (50, 5003, 4104), (3, 8193, 1096), (16, 8200, 520),
+    # K shared between workgroups, tiles of 64 with few and with many of them
+    (17, 8200, 136), (64, 8193, 1032), (40, 9000, 4104), (65, 64, 9000), (70, 200, 14336), (96, 1000, 4104),
 ]
 
 
