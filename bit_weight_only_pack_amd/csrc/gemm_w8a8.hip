@@ -239,20 +239,56 @@ __global__ __launch_bounds__(WV * 64) void w8a8_stream_kernel(W8Args p)
     w8a8_stream_rows<CH, WV, NST, XL>(p, ring, p.w + (int64_t)n0 * p.K, p.ws + n0, 0, p.rows, n0);
 }
 
-// By expert: 16 rows at a time, eight where there are no more
+// By expert.  Row y < E of the grid is expert y's first 16 rows (or eight, where
+// there are no more); the rows behind them, where an expert has more, are cut
+// into runs of 16 that the remaining rows of the grid share.  They search the
+// runs; the others, whose rows are most or all there are, start at once (128
+// experts of 1536 x 2048, one row each: 45 us, 57 with the search in all).
 template <int CH, int WV, int NST>
 __global__ __launch_bounds__(WV * 64) void w8a8_stream_experts_kernel(W8Args p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t ring[kRingBytes<CH, WV, NST, 2>];
-    const int e = blockIdx.y, n0 = blockIdx.x * CH;
-    const int last = min(p.offsets[e + 1], p.rows);
-    const int64_t row = (int64_t)e * p.N + n0;
-    for (int m0 = max(p.offsets[e], 0); m0 < last; m0 += 16) {
-        if (last - m0 > 8)
-            w8a8_stream_rows<CH, WV, NST, 2>(p, ring, p.w + row * p.K, p.ws + row, m0, min(m0 + 16, last), n0);
+    const int n0 = blockIdx.x * CH, lane = threadIdx.x & 63;
+    auto at = [&](int e) __attribute__((always_inline)) { return min(max(p.offsets[min(e, p.E)], 0), p.rows); };
+    auto run = [&](int e, int first, int last) __attribute__((always_inline)) {
+        const int64_t row = (int64_t)e * p.N + n0;
+        if (last - first > 8)
+            w8a8_stream_rows<CH, WV, NST, 2>(p, ring, p.w + row * p.K, p.ws + row, first, min(first + 16, last), n0);
         else
-            w8a8_stream_rows<CH, WV, NST, 1>(p, ring, p.w + row * p.K, p.ws + row, m0, last, n0);
-        if (m0 + 16 < last) __syncthreads();          // the sums are read before the next rows' rings are filled
+            w8a8_stream_rows<CH, WV, NST, 1>(p, ring, p.w + row * p.K, p.ws + row, first, last, n0);
+    };
+    int e = blockIdx.y, first, last, next = e - p.E;
+    if (next < 0) {
+        first = at(e);
+        last = at(e + 1);
+        if (first < last) run(e, first, last);
+        return;
+    }
+    for (;; next += gridDim.y - p.E) {
+        // run `next`: 64 experts at a time, one a lane
+        int in = next;
+        bool found = false;
+        for (int e0 = 0; e0 < p.E && !found; e0 += 64) {
+            const int low = at(e0 + lane), high = at(e0 + lane + 1), mine = max((high - low + 15) / 16 - 1, 0);
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int all = __builtin_amdgcn_readlane(incl, 63);
+            if (in < all) {
+                const int l = __ffsll((unsigned long long)__ballot(incl > in)) - 1;
+                e = e0 + l;
+                first = __builtin_amdgcn_readlane(low, l) + 16 * (in - __builtin_amdgcn_readlane(incl - mine, l) + 1);
+                last = __builtin_amdgcn_readlane(high, l);
+                found = true;
+            }
+            in -= all;
+        }
+        if (!found) return;
+        run(e, first, last);
+        __syncthreads();                              // the sums are read before the next rows' rings are filled
     }
 }
 
@@ -768,7 +804,10 @@ void stream(const W8Args &a, hipStream_t s)
 template <int CH, int WV, int NST>
 void stream_experts(const W8Args &a, hipStream_t s)
 {
-    w8a8_stream_experts_kernel<CH, WV, NST><<<dim3((a.N + CH - 1) / CH, a.E), WV * 64, 0, s>>>(a);
+    // for the runs behind the experts' first: eight, or one for every eight runs there may be (rows past the tile
+    // kernel's reach can be many: a grid has fewer than 2^16 rows)
+    const int more = min(a.rows / 16, max(8, min(a.rows / 128, 1 << 15)));
+    w8a8_stream_experts_kernel<CH, WV, NST><<<dim3((a.N + CH - 1) / CH, a.E + more), WV * 64, 0, s>>>(a);
 }
 
 template <int B, int NW, W8Mode MODE>
@@ -866,17 +905,18 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 // The kernel goes by the rows that an expert has on average, each with both
 // sides measured (us):
 //   rows an expert                            1        4        8       12       16
-//   128 experts of 1536 x 2048: stream       45       63       65       72       85
-//                               tiles of 64  56       76       79       82       84
-//   8 experts of 4096 x 4096:   stream       15       27       28       30       35
+//   128 experts of 1536 x 2048: stream       45       64       66       77       85
+//                               tiles of 64  56       76       79       81       84
+//   8 experts of 4096 x 4096:   stream       16       27       28       30       35
 //                               tiles of 64  17       32       32       32       32
 //   rows an expert                           64                 256
 //   128 experts: tiles of 64 / 128 / 256     108 /  93 / 110    257 / 176 / 182
 //   8 experts                                 39 /  40 /  55     78 /  76 /  59
+// All 1536 rows of 128 experts with one of them: 50 (tiles of 64: 16).
 // A ring of four waves and three stages holds twelve units of K: with fewer of
 // them two waves and two stages serve more workgroups a CU (128 experts of
-// 2048 x 768, 1 / 4 / 8 rows each: 25 / 35 / 36 against 32 / 45 / 47; of
-// 1536 x 2048: 47 / 66 / 69 against 45 / 63 / 65).
+// 2048 x 768, 1 / 4 / 8 rows each: 24 / 35 / 36 against 34 / 47 / 50; of
+// 1536 x 2048: 46 / 66 / 69 against 45 / 64 / 66).
 hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
 {
     // the rows' offsets inside x are 32-bit in the tile kernel when they are gathered

@@ -255,6 +255,25 @@ def test_experts_parity(T, top_k, E, N, K, skew, gather, dt):
     assert_rounded(y, y64, step, DT[dt][1], "T=%d E=%d" % (T, E))
 
 
+@pytest.mark.parametrize("E,counts,N,K", [
+    (100, {5: 700}, 70, 264), (100, {3: 16, 5: 17, 63: 33, 64: 300, 70: 1, 99: 48}, 40, 1608),   # the runs of 16 rows
+    (70, {0: 8, 1: 9, 65: 400, 69: 31}, 33, 1536), (64, {63: 768}, 64, 2048), (1000, {1: 40, 998: 2000, 999: 50}, 9, 72),
+    (3, {1: 36}, 100, 3000), (2, {0: 24}, 50, 64),
+])
+@pytest.mark.parametrize("gather", [True, False])
+def test_experts_uneven(E, counts, N, K, gather):
+    """Few rows an expert on average, but many with one or some of them."""
+    rng = np.random.default_rng(E + K)
+    S = sum(counts.values())
+    offs = np.concatenate([[0], np.cumsum([counts.get(e, 0) for e in range(E)])]).astype(np.int32)
+    (xq, xs), (wq, ws) = codes(rng, S, K), codes(rng, E * N, K)
+    wq, ws = wq.reshape(E, N, K), ws.reshape(E, N) * np.float32(0.01)
+    src = rng.permutation(S).astype(np.int32) if gather else np.arange(S)
+    y64, step = experts64(xq, xs, wq, ws, src, offs)
+    y = run_experts(dev(xq), dev(xs), dev(wq), dev(ws), dev(src) if gather else None, 1, dev(offs), S, "bf16")
+    assert_rounded(y, y64, step, torch.bfloat16)
+
+
 @pytest.mark.parametrize("T", [20, 400])
 def test_experts_rows_outside_stay(T):
     """Slots without a local expert: rows behind the last one keep what they held, and so does a table cut to `rows`."""
@@ -332,7 +351,7 @@ def test_experts_one_expert_equals_the_dense_product():
 
 
 # ---------------------------------------------------------------- streams and graphs
-@pytest.mark.parametrize("M,N,K", [(1, 512, 2048), (60, 200, 4096), (300, 520, 1024)])
+@pytest.mark.parametrize("M,N,K", [(1, 512, 2048), (60, 200, 4096), (100, 200, 8192), (300, 520, 1024)])
 def test_gemm_graph_replays(M, N, K):
     """Captured once, replayed with new inputs and eager work between: every replay equals the eager bits."""
     rng = np.random.default_rng(M)
@@ -364,7 +383,7 @@ def test_gemm_two_streams_at_once():
     """Two calls in flight with a workspace each give what they give alone."""
     rng = np.random.default_rng(4)
     sets = []
-    for M, N, K in ((48, 512, 8192), (64, 300, 8200)):
+    for M, N, K in ((48, 512, 8192), (64, 300, 8200), (100, 512, 8192), (90, 300, 8200)):
         (xq, xs), (wq, ws) = codes(rng, M, K), codes(rng, N, K)
         d = (dev(xq), dev(xs), dev(wq), dev(ws))
         nb = lb.lowbit_gemm_w8a8_workspace_bytes(M, N, K)
@@ -378,6 +397,42 @@ def test_gemm_two_streams_at_once():
     torch.cuda.synchronize()
     for s in sets:
         assert torch.equal(s[6].view(torch.int16), s[7].view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [6, 300])
+def test_experts_graph_replays(T):
+    """Captured with the sorting before it, replayed on new routings: every replay equals the eager bits."""
+    E, N, K, top_k = 12, 200, 520, 3
+    rng = np.random.default_rng(T)
+    (xq, xs), (wq, ws) = codes(rng, T, K), codes(rng, E * N, K)
+    dx, dxs, dw, dws = dev(xq), dev(xs), dev(wq.reshape(E, N, K)), dev(ws.reshape(E, N))
+    S = T * top_k
+    ids, (rs, sr, of) = dev(routing(rng, T, E, top_k)), [torch.empty(n, dtype=torch.int32, device="cuda")
+                                                         for n in (S, S, E + 1)]
+    y = torch.empty((S, N), dtype=torch.float16, device="cuda")
+    assert lb.lowbit_moe_sort_workspace_bytes(T, top_k, E) == 0
+
+    def calls(st):
+        lb.check(lb.lowbit_moe_sort(ids, T, top_k, E, None, E, rs, sr, of, None, 0, st))
+        lb.check(lb.lowbit_moe_gemm_w8a8(E, N, K, dw, dws, dx, dxs, T, rs, top_k, of, S, y, lb.LOWBIT_F16, st))
+
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            calls(stream.cuda_stream)
+    for rep in range(3):
+        ids.copy_(torch.from_numpy(routing(rng, T, E, top_k, 2.0 * rep)))
+        torch.cuda.synchronize()
+        calls(None)
+        torch.cuda.synchronize()
+        eager = y.clone()
+        y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), eager.view(torch.int16))
 
 
 # ---------------------------------------------------------------- the operators together
