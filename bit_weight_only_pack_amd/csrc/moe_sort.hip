@@ -11,6 +11,7 @@
 // The gradient of permute is unpermute without weights (each token's copies
 // added up).  Nothing is added with atomics: every output has one writer and a
 // fixed order of summation, in fp32.
+#include <algorithm>
 #include <type_traits>
 
 #include "w8a8_sort.hpp"
@@ -216,6 +217,14 @@ int row_shift(int64_t items)
     return s;
 }
 
+// Workgroups along a row: one for each of its steps where the rows are few, as nothing else hides a step's latency
+// (permute / unpermute, us: 64 tokens with 2 rows of 16 KiB 3.8 / 5.1 -> 2.8 / 2.9, 333 with 2 of 8 KiB 3.9 / 4.5 ->
+// 3.8 / 3.7); one for all where they are many (8192 with 2 of 8 KiB: 43 / 37, 43 / 40 with two).
+unsigned row_blocks(int items, int shift, bool far)
+{
+    return far ? 1 : (unsigned)std::max(1, std::min((items + (1 << shift) - 1) >> shift, 1024));
+}
+
 // Rows that no cache will hold until they are used go past it.  Measured at
 // 65536 rows of 4 KiB (us, plain / past the caches): permute 59 / 51, unpermute
 // 58 / 50, its gradient 111 / 99.
@@ -254,13 +263,13 @@ void moe_permute_kernel(const V *x, const float *x_scale, int T, int top_k, int 
 {
     const int64_t t = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
     if (t >= T) return;
-    const int c0 = threadIdx.x & ((1 << shift) - 1);
+    const int c0 = (blockIdx.y << shift) + (threadIdx.x & ((1 << shift) - 1)), step = gridDim.y << shift;
     const bool scaled = x_scale != nullptr && c0 == 0;
     const float scale = scaled ? x_scale[t] : 0.f;
     for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
         int r[kRowBatch];
         batch_rows(slot_row + t * top_k, j0, top_k, (int64_t)T * top_k, r);
-        for (int c = c0; c < items; c += 1 << shift) {
+        for (int c = c0; c < items; c += step) {
             const V v = x[t * items + c];
 #pragma unroll
             for (int j = 0; j < kRowBatch; ++j)
@@ -286,7 +295,8 @@ void moe_unpermute_kernel(const typename Elem<BF16>::v8 *yp, const float *w, int
     typedef typename Elem<BF16>::t T1;
     const int64_t t = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
     if (t >= T) return;
-    for (int c = threadIdx.x & ((1 << shift) - 1); c < items; c += 1 << shift) {
+    const int step = gridDim.y << shift;
+    for (int c = (blockIdx.y << shift) + (threadIdx.x & ((1 << shift) - 1)); c < items; c += step) {
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int j0 = 0; j0 < top_k; j0 += kRowBatch) {
             int r[kRowBatch];
@@ -413,7 +423,7 @@ hipError_t launch_moe_permute(const void *x, const float *x_scale, int T, int to
     const unsigned blocks = (unsigned)(((int64_t)T + (256 >> shift) - 1) >> (8 - shift));
     auto launch = [&](auto kernel, auto item) {
         typedef decltype(item) V;
-        kernel<<<blocks, kRowThreads, 0, s>>>(static_cast<const V *>(x), x_scale, T, top_k, items, shift, slot_row,
+        kernel<<<dim3(blocks, row_blocks(items, shift, far)), kRowThreads, 0, s>>>(static_cast<const V *>(x), x_scale, T, top_k, items, shift, slot_row,
                                               static_cast<V *>(xp), xp_scale);
         return hipGetLastError();
     };
@@ -429,7 +439,7 @@ hipError_t launch_moe_unpermute(const void *yp, int bf16, const float *w, int T,
     const unsigned blocks = (unsigned)(((int64_t)T + (256 >> shift) - 1) >> (8 - shift));
     auto launch = [&](auto kernel, auto item) {
         typedef decltype(item) v8;
-        kernel<<<blocks, kRowThreads, 0, s>>>(static_cast<const v8 *>(yp), w, T, top_k, items, shift, slot_row,
+        kernel<<<dim3(blocks, row_blocks(items, shift, far)), kRowThreads, 0, s>>>(static_cast<const v8 *>(yp), w, T, top_k, items, shift, slot_row,
                                               static_cast<v8 *>(y));
         return hipGetLastError();
     };
@@ -451,7 +461,8 @@ hipError_t launch_moe_unpermute_backward(const void *dy, const void *yp, int bf1
     };
     auto pick = [&](auto b, auto item) {
         constexpr bool B = decltype(b)::value;
-        // as many waves as have a piece of the row, up to four
+        // as many waves as have a piece of the row, up to four (eight for rows of 8 KiB: 1000 tokens of 2 rows 11.3 us
+        // for 8.6, 8192 86 for 64)
         if (items <= 64)
             return far ? launch(moe_unpermute_backward_kernel<true, B, 1>, 1, item)
                        : launch(moe_unpermute_backward_kernel<false, B, 1>, 1, item);
