@@ -355,12 +355,22 @@ __device__ __forceinline__ bool expert_tile(const W8Args &p, W8Tile &t)
 // DENSE, SPLIT: K over workgroups, int32 partial sums out; EXPERTS: rows by expert
 enum W8Mode { DENSE, SPLIT, EXPERTS };
 
+// What a tile's workgroup keeps in LDS
+template <int BM, int BN, int NW>
+struct W8Shared {
+    static constexpr int NST = BM * BN == 64 * 64 ? 4 : 2;   // LDS stages
+    static constexpr int NS = (BM + 2 * BN + NW * 64 - 1) / (NW * 64);
+    __attribute__((aligned(1024))) uint8_t stages[NST * (BM + BN) * 32 * NW];
+    __attribute__((aligned(16))) float sc[NS * NW * 64];      // token scales, channel scales, biases
+};
+
+// tile t, K steps s0 .. s1 - 1 of BK bytes
 template <int BM, int BN, int NW, W8Mode MODE>
-__global__ __launch_bounds__(NW * 64, 1)
-void w8a8_tile_kernel(W8Args p)
+__device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const int s0, const int s1, const int split,
+                                          uint8_t *stages, float *sc)
 {
-    constexpr int NST = BM * BN == 64 * 64 ? 4 : 2;   // LDS stages
-    constexpr int BK = 32 * NW;                       // bytes of K in one
+    constexpr int NST = W8Shared<BM, BN, NW>::NST;
+    constexpr int BK = 32 * NW;                       // bytes of K in a stage
     // 64 x 64: each wave has the whole tile and 32 bytes of every stage's K, so that no operand is read from LDS
     // twice; otherwise each has a quarter of the tile.
     constexpr bool KW = BM * BN == 64 * 64;
@@ -372,39 +382,12 @@ void w8a8_tile_kernel(W8Args p)
     constexpr int STAGE = (BM + BN) * BK;
     constexpr int SAME = 256 / BK;                    // rows in 256 bytes: all of LDS's banks
     static_assert(RPL * NW / SAME % C16 == 0, "every load stores its chunks in the same order");
-    __shared__ __attribute__((aligned(1024))) uint8_t stages[NST * STAGE];
-    constexpr int THREADS = NW * 64, NS = (BM + 2 * BN + THREADS - 1) / THREADS;
-    __shared__ __attribute__((aligned(16))) float sc[NS * THREADS];   // token scales, channel scales, biases
+    constexpr int THREADS = NW * 64, NS = W8Shared<BM, BN, NW>::NS;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = KW ? 0 : wave & 1, wc = KW ? 0 : wave >> 1;
-    W8Tile t;
-    const int full = p.K / BK, steps = KW || full * BK == p.K ? full : full + 1;
-    int s0 = 0, s1 = (steps + 1) / 2 * 2, split = 0;  // steps, in pairs
-    if constexpr (MODE == EXPERTS) {
-        if (!expert_tile<BM, BN>(p, t)) return;
-    } else {
-        // each XCD takes a run of tiles, which covers blocks of 8 token tiles
-        const uint32_t mt = (p.rows + BM - 1) / BM, nt = (p.N + BN - 1) / BN;
-        const uint32_t tiles = mt * nt, all = MODE == SPLIT ? tiles * p.splits : tiles, per = (all + 7) / 8;
-        const uint32_t slot = blockIdx.x >> 3, lin = (blockIdx.x & 7) * per + slot;
-        if (slot >= per || lin >= all) return;
-        uint32_t in = lin;
-        if constexpr (MODE == SPLIT) {
-            split = lin / tiles;
-            in = lin % tiles;
-            const int pairs = s1 / 2;
-            s0 = (int)((int64_t)pairs * split / p.splits) * 2;
-            s1 = (int)((int64_t)pairs * (split + 1) / p.splits) * 2;
-        }
-        const uint32_t group = in / (8 * nt);
-        const uint32_t high = min(8u, mt - group * 8), rest = in - group * 8 * nt;
-        t.e = 0;
-        t.first = (group * 8 + rest % high) * BM;
-        t.last = p.rows;
-        t.n0 = rest / high * BN;
-    }
+    const int full = p.K / BK;
     const int m_valid = min(BM, t.last - t.first), n_valid = min(BN, p.N - t.n0);
     const int8_t *xb = MODE == EXPERTS && p.row_slot ? p.x : p.x + (int64_t)t.first * p.K;
     const int8_t *wb = p.w + ((int64_t)t.e * p.N + t.n0) * p.K;
@@ -464,15 +447,16 @@ void w8a8_tile_kernel(W8Args p)
     // the step that K ends inside, or an empty one that makes up a pair: bytes past K are zeros
     auto load_tail = [&](int s, uint8_t *buf) __attribute__((always_inline)) {
         const int k = s * BK + chunk0 * 16;
+        constexpr int G = (LX + LW) % 4 == 0 ? 4 : 2;
 #pragma unroll
-        for (int j = 0; j < LX + LW; j += 4) {
-            i4 v[4];
+        for (int j = 0; j < LX + LW; j += G) {
+            i4 v[G];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < G; ++i)
                 v[i] = !KW && s * BK < p.K ? row16((j + i < LX ? xb : wb) + (off[j + i] - chunk0 * 16), k, p.K)
                                         : i4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<i4 *>(place(buf, j + i) + lane * 16) = v[i];
+            for (int i = 0; i < G; ++i) *reinterpret_cast<i4 *>(place(buf, j + i) + lane * 16) = v[i];
         }
     };
     auto load_stage = [&](int s, uint8_t *buf) __attribute__((always_inline)) {
@@ -730,6 +714,50 @@ void w8a8_tile_kernel(W8Args p)
             }
         }
     }
+}
+
+template <int BM, int BN, int NW, W8Mode MODE>
+__global__ __launch_bounds__(NW * 64, 1)
+void w8a8_tile_kernel(W8Args p)
+{
+    __shared__ W8Shared<BM, BN, NW> sh;
+    W8Tile t;
+    // K in steps of BK bytes, in pairs; tiles of 64 take its end on their own
+    constexpr int BK = 32 * NW;
+    const int full = p.K / BK, steps = BM * BN == 64 * 64 || full * BK == p.K ? full : full + 1;
+    int s0 = 0, s1 = (steps + 1) / 2 * 2, split = 0;
+    if constexpr (MODE == EXPERTS) {
+        if (!expert_tile<BM, BN>(p, t)) return;
+    } else {
+        // each XCD takes a run of tiles, which covers blocks of 8 token tiles
+        const uint32_t mt = (p.rows + BM - 1) / BM, nt = (p.N + BN - 1) / BN;
+        const uint32_t tiles = mt * nt, all = MODE == SPLIT ? tiles * p.splits : tiles, per = (all + 7) / 8;
+        const uint32_t slot = blockIdx.x >> 3, lin = (blockIdx.x & 7) * per + slot;
+        if (slot >= per || lin >= all) return;
+        uint32_t in = lin;
+        if constexpr (MODE == SPLIT) {
+            split = lin / tiles;
+            in = lin % tiles;
+            const int pairs = s1 / 2;
+            s0 = (int)((int64_t)pairs * split / p.splits) * 2;
+            s1 = (int)((int64_t)pairs * (split + 1) / p.splits) * 2;
+        }
+        const uint32_t group = in / (8 * nt);
+        const uint32_t high = min(8u, mt - group * 8), rest = in - group * 8 * nt;
+        t.e = 0;
+        t.first = (group * 8 + rest % high) * BM;
+        t.last = p.rows;
+        t.n0 = rest / high * BN;
+    }
+    // An expert's last tile with half its rows or fewer is done as half a tile: it moves fewer bytes and multiplies half
+    // as much (128 experts of 1536 x 2048, us: 128 rows each 133 in tiles of 128 and 129 in tiles of 256, 143 and 142
+    // without; 256 rows 217 and 235, 221 and 249).
+    if constexpr (MODE == EXPERTS && BM > 64)
+        if (t.last - t.first <= BM / 2) {
+            w8a8_tile<BM / 2, BN, NW, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
+            return;
+        }
+    w8a8_tile<BM, BN, NW, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
 }
 
 // Sums of the splits' planes, in their order, scaled and rounded: V values of a row a thread
