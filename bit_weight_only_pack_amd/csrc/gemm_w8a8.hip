@@ -34,19 +34,30 @@ __device__ __forceinline__ void put(void *y, int64_t o, float v, int bf16)
         static_cast<_Float16 *>(y)[o] = (_Float16)v;
 }
 
-__device__ __forceinline__ void put8(void *y, int64_t o, const float *v, int bf16)
+// Vectors of outputs and partial sums start at any element: rows of odd lengths
+// are stored 16 bytes at a time too (global memory takes them at any address).
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef b8 b8_any __attribute__((aligned(2)));
+typedef h8 h8_any __attribute__((aligned(2)));
+typedef i4 i4_any __attribute__((aligned(4)));
+
+// outputs o .. o + 7, the first `valid` of them
+__device__ __forceinline__ void put8(void *y, int64_t o, const float *v, int valid, int bf16)
 {
-    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-    if (bf16) {
+    if (valid < 8) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < valid) put(y, o + i, v[i], bf16);
+    } else if (bf16) {
         b8 r;
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[i];
-        *reinterpret_cast<b8 *>(static_cast<__bf16 *>(y) + o) = r;
+        *reinterpret_cast<b8_any *>(static_cast<__bf16 *>(y) + o) = r;
     } else {
         h8 r;
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[i] = (_Float16)v[i];
-        *reinterpret_cast<h8 *>(static_cast<_Float16 *>(y) + o) = r;
+        *reinterpret_cast<h8_any *>(static_cast<_Float16 *>(y) + o) = r;
     }
 }
 
@@ -213,6 +224,7 @@ __device__ __forceinline__ void w8a8_stream_rows(const W8Args &p, uint8_t *ring,
 
     __syncthreads();                                  // every ring is done with
     int *part = reinterpret_cast<int *>(ring);        // [waves][16 TB][CH]
+    static_assert(THREADS % CH == 0, "a thread finishes sums of one channel");
     static_assert(WV * 16 * TB * CH * 4 <= kRingBytes<CH, WV, NST, XL>, "the sums fit the rings");
 #pragma unroll
     for (int t = 0; t < TB; ++t)
@@ -637,8 +649,6 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
             ws[h] = *reinterpret_cast<const f4 *>(&sc[BM + n + 4 * h]);
             bs[h] = *reinterpret_cast<const f4 *>(&sc[BM + BN + n + 4 * h]);
         }
-    const bool wide = MODE == SPLIT ? (p.N & 3) == 0
-                                    : (p.N & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
     auto stash = [&](int b, uint8_t *region) __attribute__((always_inline)) {
 #pragma unroll
         for (int c = 0; c < TC; ++c)
@@ -658,51 +668,34 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
             int32_t *to = p.part + (int64_t)split * p.rows * p.N + o;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (n + 4 * h < n_valid) *reinterpret_cast<i4 *>(to + 4 * h) = v[h];
+                if (n + 4 * h + 4 <= n_valid) {
+                    *reinterpret_cast<i4_any *>(to + 4 * h) = v[h];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        if (n + 4 * h + i < n_valid) to[4 * h + i] = v[h][i];
+                }
         } else {
             const float xs = sc[tok];
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = (float)v[i / 4][i % 4] * xs * ws[i / 4][i % 4] + bs[i / 4][i % 4];
-            if (n < n_valid) put8(p.y, o, f, p.y_bf16);
+            put8(p.y, o, f, n_valid - n, p.y_bf16);
         }
-    };
-    // rows that start anywhere: value by value, neighbouring lanes neighbouring channels (623 x 23755 of K = 280
-    // in 30 us; 38 with a lane's eight in turn)
-    auto fetch1 = [&](const uint8_t *region, int r, int c) __attribute__((always_inline)) {
-        return *reinterpret_cast<const int *>(region + r * (CW * 4) + ((c / 4 ^ (r & (CHUNKS - 1))) * 16) + c % 4 * 4);
-    };
-    auto emit1 = [&](int tok, int c, int v) __attribute__((always_inline)) {
-        if (tok >= m_valid || c >= n_valid) return;
-        const int64_t o = (int64_t)(t.first + tok) * p.N + t.n0 + c;
-        if constexpr (MODE == SPLIT)
-            p.part[(int64_t)split * p.rows * p.N + o] = v;
-        else
-            put(p.y, o, (float)v * sc[tok] * sc[BM + c] + sc[BM + BN + c], p.y_bf16);
     };
     if constexpr (KW) {
         // every wave's sums of the tile; then eight lanes add up and finish a row
 #pragma unroll
         for (int b = 0; b < TT; ++b) stash(b, stages + (wave * TT + b) * REGION);
         sync(std::integral_constant<int, 0>{});
-        if (wide) {
 #pragma unroll
-            for (int row = tid / 8; row < BM; row += THREADS / 8) {
-                i4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        for (int row = tid / 8; row < BM; row += THREADS / 8) {
+            i4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-                for (int q = 0; q < NW; ++q)
+            for (int q = 0; q < NW; ++q)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) v[h] += fetch(stages + (q * TT + row / 32) * REGION, row % 32, h);
-                emit(row, v);
-            }
-        } else {
-#pragma unroll 2
-            for (int row = wave; row < BM; row += NW) {
-                int v = 0;
-#pragma unroll
-                for (int q = 0; q < NW; ++q) v += fetch1(stages + (q * TT + row / 32) * REGION, row % 32, lane);
-                emit1(row, lane, v);
-            }
+                for (int h = 0; h < 2; ++h) v[h] += fetch(stages + (q * TT + row / 32) * REGION, row % 32, h);
+            emit(row, v);
         }
     } else {
         uint8_t *mine = stages + wave * REGION;
@@ -711,18 +704,10 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
         for (int b = 0; b < TT; ++b) {
             const int tok0 = (wt * TT + b) * 32;
             stash(b, mine);
-            if (wide) {
 #pragma unroll 4
-                for (int r = lane / (CW / 8); r < 32; r += RSTEP) {
-                    const i4 v[2] = {fetch(mine, r, 0), fetch(mine, r, 1)};
-                    emit(tok0 + r, v);
-                }
-            } else {
-#pragma unroll 4
-                for (int i = 0; i < 32 * CW / 64; ++i) {
-                    const int r = i / (CW / 64), c = i % (CW / 64) * 64 + lane;
-                    emit1(tok0 + r, wc * CW + c, fetch1(mine, r, c));
-                }
+            for (int r = lane / (CW / 8); r < 32; r += RSTEP) {
+                const i4 v[2] = {fetch(mine, r, 0), fetch(mine, r, 1)};
+                emit(tok0 + r, v);
             }
         }
     }
@@ -772,40 +757,43 @@ void w8a8_tile_kernel(W8Args p)
     w8a8_tile<BM, BN, NW, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
 }
 
-// Sums of the splits' planes, in their order, scaled and rounded: V values of a row a thread
-template <int V>
+// Sums of the splits' planes, in their order, scaled and rounded: four channels of a row a thread
 __global__ __launch_bounds__(256) void w8a8_reduce_kernel(W8Args p)
 {
-    const int64_t MN = (int64_t)p.rows * p.N, o = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-    if (o >= MN) return;
-    typedef int iv __attribute__((ext_vector_type(V)));
-    typedef float fv __attribute__((ext_vector_type(V)));
-    iv s = *reinterpret_cast<const iv *>(p.part + o);
-    for (int q = 1; q < p.splits; ++q) s += *reinterpret_cast<const iv *>(p.part + q * MN + o);
-    const int m = (int)(o / p.N), n = (int)(o - (int64_t)m * p.N);
+    const int64_t MN = (int64_t)p.rows * p.N, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int groups = (p.N + 3) / 4;
+    if (i >= (int64_t)p.rows * groups) return;
+    const int m = (int)(i / groups), n = (int)(i - (int64_t)m * groups) * 4;
+    const int64_t o = (int64_t)m * p.N + n;
     const float xs = p.xs[m];
-    fv v;
+    if (n + 4 <= p.N) {
+        i4 s = *reinterpret_cast<const i4_any *>(p.part + o);
+        for (int q = 1; q < p.splits; ++q) s += *reinterpret_cast<const i4_any *>(p.part + q * MN + o);
+        f4 v;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        v[i] = (float)s[i] * xs * p.ws[n + i];
-        if (p.bias) v[i] += p.bias[n + i];
+        for (int j = 0; j < 4; ++j) v[j] = (float)s[j] * xs * p.ws[n + j] + (p.bias ? p.bias[n + j] : 0.f);
+        if (p.y_bf16) {
+            typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+            typedef b4 b4_any __attribute__((aligned(2)));
+            *reinterpret_cast<b4_any *>(static_cast<__bf16 *>(p.y) + o) = __builtin_convertvector(v, b4);
+        } else {
+            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+            typedef h4 h4_any __attribute__((aligned(2)));
+            *reinterpret_cast<h4_any *>(static_cast<_Float16 *>(p.y) + o) = __builtin_convertvector(v, h4);
+        }
+        return;
     }
-    if (p.y_bf16) {
-        typedef __bf16 bv __attribute__((ext_vector_type(V)));
-        *reinterpret_cast<bv *>(static_cast<__bf16 *>(p.y) + o) = __builtin_convertvector(v, bv);
-    } else {
-        typedef _Float16 hv __attribute__((ext_vector_type(V)));
-        *reinterpret_cast<hv *>(static_cast<_Float16 *>(p.y) + o) = __builtin_convertvector(v, hv);
+    for (int j = 0; n + j < p.N; ++j) {
+        int s = p.part[o + j];
+        for (int q = 1; q < p.splits; ++q) s += p.part[q * MN + o + j];
+        put(p.y, o + j, (float)s * xs * p.ws[n + j] + (p.bias ? p.bias[n + j] : 0.f), p.y_bf16);
     }
 }
 
 void reduce_launch(const W8Args &a, hipStream_t s)
 {
-    const int64_t MN = (int64_t)a.rows * a.N;
-    if (a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0)
-        w8a8_reduce_kernel<4><<<(unsigned)((MN / 4 + 255) / 256), 256, 0, s>>>(a);
-    else
-        w8a8_reduce_kernel<1><<<(unsigned)((MN + 255) / 256), 256, 0, s>>>(a);
+    const int64_t threads = (int64_t)a.rows * ((a.N + 3) / 4);
+    w8a8_reduce_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a);
 }
 
 }  // namespace
