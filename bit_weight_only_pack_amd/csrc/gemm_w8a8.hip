@@ -14,6 +14,7 @@
 // v_mfma_i32_16x16x64_i8 (lane l: row l % 16, K bytes 16 (l / 16) .. + 15), so
 // weights need no re-packing.  The weight is the A operand and the activation
 // the B operand: a lane then holds four consecutive channels of one token.
+#include <algorithm>
 #include <type_traits>
 
 #include "w8a8_sort.hpp"
@@ -865,27 +866,37 @@ struct W8Plan {
 // workgroups of one launch: a grid holds fewer than 2^32 threads
 constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 
-// The tile size and split with the least estimated time: a start and an end,
-// then per 128 bytes of K a time for each tile a CU has to take (one tile of
-// 64 x 64 does not fill a CU).  A split adds the pass over the partial sums.
+// Estimated time (us) of a launch of tiles: a start and an end, then per 128
+// bytes of K a time for each tile a CU has to take, another one where it has no
+// more than one.  The constants are fitted to the choice among 2300 measured
+// launches (195 shapes of 371 to 28672 channels, K 192 to 14336 and 69 to 4096
+// rows; each tile size unsplit and split): it takes 0.3 % longer than the best
+// of them on average and 19 % at most.
+struct W8Cost {
+    int size;
+    double ends, step, alone;
+};
+constexpr W8Cost kCosts[] = {{64, 4.7, 0.28, 0.12}, {128, 4.4, 0.55, 0.87}, {256, 17.2, 1.68, 1.14}};
+
+double tiles_time(const W8Cost &c, int64_t tiles, int pairs)
+{
+    const int64_t each = (tiles + kCUs - 1) / kCUs;
+    return c.ends + pairs * 2 * (each > 1 ? each * c.step : c.alone);
+}
+
+// The tile size and split with the least estimated time.  A split adds the pass
+// over the partial sums.
 W8Plan w8_plan(int rows, int N, int K)
 {
-    struct Cost {
-        int size;
-        double ends, step, least;                     // microseconds
-    };
-    constexpr Cost kCosts[] = {{64, 5.5, 0.25, 0.15}, {128, 6.0, 0.56, 0.56}, {256, 14.0, 1.6, 1.6}};
     const int pairs = (K + 255) / 256;
     W8Plan best = {64, 1, 0};
     double time = -1.0;
-    for (const Cost &c : kCosts) {
+    for (const W8Cost &c : kCosts) {
         const int64_t tiles = (((int64_t)rows + c.size - 1) / c.size) * (((int64_t)N + c.size - 1) / c.size);
         if (tiles >= kMaxTiles && c.size < 256) continue;
         for (int splits = 1; splits <= 8 && (splits == 1 || splits * 2 <= pairs); splits *= 2) {
-            const int64_t each = (tiles * splits + kCUs - 1) / kCUs;
-            const double step = each > 1 ? each * c.step : c.least;
-            const double reduce = splits > 1 ? 3.0 + (double)splits * rows * N * 8 / 4e6 : 0.0;
-            const double us = c.ends + (pairs + splits - 1) / splits * 2 * step + reduce;
+            const double reduce = splits > 1 ? 2.4 + (double)splits * rows * N * 8 / 4.2e6 : 0.0;
+            const double us = tiles_time(c, tiles * splits, (pairs + splits - 1) / splits) + reduce;
             if (time < 0.0 || us < time) {
                 time = us;
                 best = {c.size, splits, tiles * splits};
@@ -930,8 +941,8 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
     return hipGetLastError();
 }
 
-// The kernel goes by the rows that an expert has on average, each with both
-// sides measured (us):
+// Streaming goes by the rows that an expert has on average, tiles by their
+// estimated time; both sides measured (us):
 //   rows an expert                            1        4        8       12       16
 //   128 experts of 1536 x 2048: stream       45       64       66       77       85
 //                               tiles of 64  56       76       79       81       84
@@ -939,7 +950,7 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 //                               tiles of 64  17       32       32       32       32
 //   rows an expert                           64                 256
 //   128 experts: tiles of 64 / 128 / 256     108 /  93 / 110    257 / 176 / 182
-//   8 experts                                 39 /  40 /  55     78 /  76 /  59
+//   8 experts                                 39 /  38 /  48     78 /  74 /  61
 // All 1536 rows of 128 experts with one of them: 50 (tiles of 64: 16).
 // A ring of four waves and three stages holds twelve units of K: with fewer of
 // them two waves and two stages serve more workgroups a CU (128 experts of
@@ -956,11 +967,21 @@ hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
             stream_experts<32, 4, 3>(a, s);
         return hipGetLastError();
     }
-    int size = a.rows < 64 * a.E ? 64 : a.rows < 256 * a.E || a.K < 4096 ? 128 : 256;
-    // an expert's last tile is not full: at most one more for each of them
-    auto tiles = [&]() { return ((int64_t)a.rows / size + a.E) * (((int64_t)a.N + size - 1) / size); };
-    while (tiles() >= kMaxTiles && size < 256) size *= 2;
-    tile_launch<EXPERTS>(a, size, tiles(), s);
+    // the size whose tiles take the least estimated time, an expert's last tile being half full and every expert
+    // having a row; at most one more tile for each of them is launched
+    int size = 0;
+    double time = 0.0;
+    auto tiles = [&](int size) { return ((int64_t)a.rows / size + a.E) * (((int64_t)a.N + size - 1) / size); };
+    for (const W8Cost &c : kCosts) {
+        if (tiles(c.size) >= kMaxTiles && c.size < 256) continue;
+        const int64_t likely = std::max((int64_t)a.E, (int64_t)a.rows / c.size + a.E / 2);
+        const double us = tiles_time(c, likely * ((a.N + c.size - 1) / c.size), (a.K + 255) / 256);
+        if (size == 0 || us < time) {
+            time = us;
+            size = c.size;
+        }
+    }
+    tile_launch<EXPERTS>(a, size, tiles(size), s);
     return hipGetLastError();
 }
 
