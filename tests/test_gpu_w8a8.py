@@ -83,9 +83,14 @@ def test_gemm_parity(M, N, K, dt, bias):
     assert_rounded(y, y64, step, DT[dt][1], "M=%d N=%d K=%d" % (M, N, K))
 
 
-@pytest.mark.parametrize("M,N,K", [(4090, 4095, 8200), (4096, 4096, 4096), (700, 9000, 520)])
+@pytest.mark.parametrize("M,N,K", [
+    (4090, 4095, 8200), (4096, 4096, 4096), (700, 9000, 520),
+    # tiles of 64 (more than one a CU), 128, 256; K shared by 2, 4 and 8 workgroups in tiles of 64, 128 and 256
+    (150, 6001, 200), (70, 9001, 208), (1500, 1502, 200), (3000, 4097, 2056), (24, 20567, 20384), (1500, 1501, 8200),
+    (70, 9001, 4104), (70, 9002, 14328), (1001, 4097, 8200), (150, 9001, 14328),
+])
 def test_gemm_large(M, N, K):
-    """Sizes of the widest tiles, ragged and not; the 64-bit product on the GPU, all values."""
+    """Sizes of the wider tiles, ragged and not; the 64-bit product on the GPU, all values."""
     g = torch.Generator(device="cuda").manual_seed(M + K)
     xq = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
     wq = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
@@ -272,6 +277,36 @@ def test_experts_uneven(E, counts, N, K, gather):
     y64, step = experts64(xq, xs, wq, ws, src, offs)
     y = run_experts(dev(xq), dev(xs), dev(wq), dev(ws), dev(src) if gather else None, 1, dev(offs), S, "bf16")
     assert_rounded(y, y64, step, torch.bfloat16)
+
+
+@pytest.mark.parametrize("counts,E,N,K", [
+    ({0: 256, 3: 257, 90: 64, 91: 65, 92: 128, 93: 129, 94: 192, 99: 209}, 100, 777, 136),     # tiles of 128
+    ({0: 1000, 5: 2064, 14: 1896, 15: 40}, 16, 333, 136),
+    ({0: 2300, 1: 1412, 2: 1288}, 3, 3001, 2056), ({0: 128, 1: 2432, 2: 2440}, 3, 3001, 2064),  # of 256
+    ({e: 20 + e for e in range(0, 40)}, 40, 333, 136),                                         # of 64
+])
+@pytest.mark.parametrize("gather,dt", [(True, "bf16"), (False, "f16")])
+def test_experts_large(counts, E, N, K, gather, dt):
+    """Rows in tiles of every width whose last one is whole, more than half full and less; 64 bits on the GPU."""
+    S = sum(counts.values())
+    g = torch.Generator(device="cuda").manual_seed(S + K)
+    offs = np.concatenate([[0], np.cumsum([counts.get(e, 0) for e in range(E)])]).astype(np.int32)
+    xq = torch.randint(-128, 128, (S, K), dtype=torch.int8, device="cuda", generator=g)
+    wq = torch.randint(-128, 128, (E, N, K), dtype=torch.int8, device="cuda", generator=g)
+    xs = torch.rand(S, device="cuda", generator=g) * 0.001
+    ws = torch.rand(E, N, device="cuda", generator=g) * 0.01
+    src = torch.randperm(S, device="cuda", generator=g)
+    if not gather:
+        src = torch.arange(S, device="cuda")
+    y = run_experts(xq, xs, wq, ws, (2 * src + 1).int() if gather else None, 2, dev(offs), S, dt)
+    dtype = DT[dt][1]
+    eps, tiny = torch.finfo(dtype).eps / 2, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+    for e in counts:
+        at = slice(int(offs[e]), int(offs[e + 1]))
+        a = src[at]
+        y64 = torch.mm(xq[a].double(), wq[e].double().t()) * xs[a].double()[:, None] * ws[e].double()[None, :]
+        step = 4.01 * U32 * y64.abs()
+        assert bool(((y[at].double() - y64).abs() <= eps * (y64.abs() + step) + step + tiny).all()), e
 
 
 @pytest.mark.parametrize("T", [20, 400])
