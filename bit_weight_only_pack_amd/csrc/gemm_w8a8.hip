@@ -71,6 +71,18 @@ __device__ __forceinline__ i4 row16(const int8_t *row, int k, int K)
     return i4{lo.x & lm, lo.y & lm, hi.x & hm, hi.y & hm};
 }
 
+// sum of the lanes' values up to and including the lane's, in registers (shuffles go through LDS)
+__device__ __forceinline__ int wave_prefix_sum(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1, :2, :4, :8 within 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, uint32_t lane_off, int k, uint8_t *lds)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)lds, 16, lane_off, k, 0, 0);
@@ -283,12 +295,7 @@ __global__ __launch_bounds__(WV * 64) void w8a8_stream_experts_kernel(W8Args p)
         bool found = false;
         for (int e0 = 0; e0 < p.E && !found; e0 += 64) {
             const int low = at(e0 + lane), high = at(e0 + lane + 1), mine = max((high - low + 15) / 16 - 1, 0);
-            int incl = mine;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int v = __shfl_up(incl, o);
-                if (lane >= o) incl += v;
-            }
+            const int incl = wave_prefix_sum(mine);
             const int all = __builtin_amdgcn_readlane(incl, 63);
             if (in < all) {
                 const int l = __ffsll((unsigned long long)__ballot(incl > in)) - 1;
@@ -333,48 +340,48 @@ struct W8Tile {
     int e, first, last, n0;
 };
 
-template <int BM, int BN>
+// P: experts a lane has, one after the other, at most.  Their offsets are loaded
+// together and stay in registers: one wait for memory (1.0 us of the 21 that a
+// tile of 128 x 128 with K = 2048 takes; 2.1 with a second look at the offsets
+// and shuffles for the sum).
+template <int BM, int BN, int P>
 __device__ __forceinline__ bool expert_tile(const W8Args &p, W8Tile &t)
 {
     const int lane = threadIdx.x & 63;
     const int nt = (p.N + BN - 1) / BN;
-    // a lane has `per` experts one after the other; all their offsets are loaded at once
     const int per = (p.E + 63) / 64, e0 = lane * per;
-    auto at = [&](int e) __attribute__((always_inline)) { return min(max(p.offsets[min(e, p.E)], 0), p.rows); };
-    int mine = 0, low = at(e0);
-    const int first = low;
-#pragma unroll 4
-    for (int i = 0; i < per; ++i) {
-        const int high = at(e0 + i + 1);
-        mine += (max(high - low, 0) + BM - 1) / BM;
-        low = high;
-    }
-    int incl = mine;
+    int at[P + 1];                                    // where the lane's experts begin, and its last one ends
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(incl, o);
-        if (lane >= o) incl += v;
+    for (int i = 0; i <= P; ++i) at[i] = p.offsets[min(e0 + min(i, per), p.E)];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i <= P; ++i) {
+        at[i] = min(max(at[i], 0), p.rows);
+        if (i > 0) mine += (max(at[i] - at[i - 1], 0) + BM - 1) / BM;
     }
+    const int incl = wave_prefix_sum(mine);
     const int total = __builtin_amdgcn_readlane(incl, 63) * nt;
     const int run = (total + 7) / 8;                  // each XCD takes a run of tiles
     const int slot = blockIdx.x >> 3, lin = (blockIdx.x & 7) * run + slot;
     if (slot >= run || lin >= total) return false;
     // the lane whose experts have it, then the expert among them
     const int l = __ffsll((unsigned long long)__ballot(incl * nt > lin)) - 1;
-    int in = lin - __builtin_amdgcn_readlane(incl - mine, l) * nt, e = l * per;
-    low = __builtin_amdgcn_readlane(first, l);
-    for (;; ++e) {
-        const int high = at(e + 1), tiles = (max(high - low, 0) + BM - 1) / BM;
-        if (in < tiles * nt) {
-            t.e = e;
-            t.first = low + in % tiles * BM;
-            t.last = high;
-            t.n0 = in / tiles * BN;
-            return true;
+    int in = lin - __builtin_amdgcn_readlane(incl - mine, l) * nt, low = 0, high = 0, tiles = 1;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (!found) {
+            low = __builtin_amdgcn_readlane(at[i], l);
+            high = __builtin_amdgcn_readlane(at[i + 1], l);
+            tiles = (max(high - low, 0) + BM - 1) / BM;
+            t.e = l * per + i;
+            found = in < tiles * nt;
+            if (!found) in -= tiles * nt;
         }
-        in -= tiles * nt;
-        low = high;
-    }
+    t.first = low + in % tiles * BM;
+    t.last = high;
+    t.n0 = in / tiles * BN;
+    return true;
 }
 
 // DENSE, SPLIT: K over workgroups, int32 partial sums out; EXPERTS: rows by expert
@@ -725,7 +732,7 @@ void w8a8_tile_kernel(W8Args p)
     const int full = p.K / BK, steps = BM * BN == 64 * 64 || full * BK == p.K ? full : full + 1;
     int s0 = 0, s1 = (steps + 1) / 2 * 2, split = 0;
     if constexpr (MODE == EXPERTS) {
-        if (!expert_tile<BM, BN>(p, t)) return;
+        if (!(p.E <= 256 ? expert_tile<BM, BN, 4>(p, t) : expert_tile<BM, BN, 16>(p, t))) return;
     } else {
         // each XCD takes a run of tiles, which covers blocks of 8 token tiles
         const uint32_t mt = (p.rows + BM - 1) / BM, nt = (p.N + BN - 1) / BN;
