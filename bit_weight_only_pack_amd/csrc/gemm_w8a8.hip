@@ -325,10 +325,14 @@ __global__ __launch_bounds__(WV * 64) void w8a8_stream_experts_kernel(W8Args p)
 //              2.5e15 operations/s), 171 with no load and no LDS read left in the
 //              loop.  Per byte brought to LDS it does twice the work of 128 x 128;
 //              one wave a SIMD, so a start and an end (14 us) that nothing hides.
-//   128 x 128  bytes from L2 to LDS: 32768 rows with 128 experts of 1536 x 2048 in
-//              188 us, 2.4 GB at 12.8e12 B/s, the matrix cores busy 29 % of the
-//              time, bytes from memory 1.09 times the least.  Two workgroups a CU
-//              hide each other's starts and ends.
+//   128 x 256  bytes from L2 to LDS, three quarters of those of 128 x 128; three
+//              stages, two waves a SIMD: 32768 rows with 128 experts of 1536 x 2048
+//              in 201 us (codes of the whole range; 204 in tiles of 128 x 128, 216
+//              in tiles of 256 x 256).
+//   128 x 128  bytes from L2 to LDS: the same product moves 2.4 GB in its 204 us,
+//              the matrix cores busy 28 % of the time, bytes from memory 1.09 times
+//              the least.  Two workgroups a CU hide each other's starts and ends,
+//              which counts where K is short (2048 x 768: 82 us, 88 in 128 x 256).
 //   64 x 64    latency: few tiles (77 x 5003 of K = 4104: 10.5 us, 158 of them), so
 //              all waves share one tile's K, and four stages are under way.
 typedef int i16v __attribute__((ext_vector_type(16)));
@@ -388,33 +392,31 @@ __device__ __forceinline__ bool expert_tile(const W8Args &p, W8Tile &t)
 enum W8Mode { DENSE, SPLIT, EXPERTS };
 
 // What a tile's workgroup keeps in LDS
-template <int BM, int BN, int NW>
+template <int BM, int BN, int NW, int BK, int NST>
 struct W8Shared {
-    static constexpr int NST = BM * BN == 64 * 64 ? 4 : 2;   // LDS stages
     static constexpr int NS = (BM + 2 * BN + NW * 64 - 1) / (NW * 64);
-    __attribute__((aligned(1024))) uint8_t stages[NST * (BM + BN) * 32 * NW];
+    __attribute__((aligned(1024))) uint8_t stages[NST * (BM + BN) * BK];
     __attribute__((aligned(16))) float sc[NS * NW * 64];      // token scales, channel scales, biases
 };
 
 // tile t, K steps s0 .. s1 - 1 of BK bytes
-template <int BM, int BN, int NW, W8Mode MODE>
+template <int BM, int BN, int NW, int BK, int NST, W8Mode MODE>
 __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const int s0, const int s1, const int split,
                                           uint8_t *stages, float *sc)
 {
-    constexpr int NST = W8Shared<BM, BN, NW>::NST;
-    constexpr int BK = 32 * NW;                       // bytes of K in a stage
     // 64 x 64: each wave has the whole tile and 32 bytes of every stage's K, so that no operand is read from LDS
-    // twice; otherwise each has a quarter of the tile.
+    // twice; otherwise the waves share its area.
     constexpr bool KW = BM * BN == 64 * 64;
-    static_assert(KW || NW == 4, "2 x 2 waves share a tile");
-    constexpr int NK = KW ? 1 : 4;                    // 32-byte pieces of a step that a wave multiplies
-    constexpr int TC = KW ? 2 : BN / 64, TT = KW ? 2 : BM / 64;   // 32-wide blocks of a wave: channels, tokens
+    static_assert(!KW || BK == 32 * NW, "a wave has 32 bytes of K");
+    constexpr int NK = KW ? 1 : BK / 32;              // 32-byte pieces of a step that a wave multiplies
+    constexpr int WC = KW ? 1 : NW / 2;               // waves side by side along the channels; two along the tokens
+    constexpr int TC = BN / 32 / WC, TT = KW ? 2 : BM / 64;   // 32-wide blocks of a wave: channels, tokens
     constexpr int C16 = BK / 16, RPL = 64 / C16;      // 16-byte chunks of a row, rows of one LDS-direct load
     constexpr int LX = BM / RPL / NW, LW = BN / RPL / NW;   // such loads of a wave per stage
     constexpr int STAGE = (BM + BN) * BK;
     constexpr int SAME = 256 / BK;                    // rows in 256 bytes: all of LDS's banks
     static_assert(RPL * NW / SAME % C16 == 0, "every load stores its chunks in the same order");
-    constexpr int THREADS = NW * 64, NS = W8Shared<BM, BN, NW>::NS;
+    constexpr int THREADS = NW * 64, NS = W8Shared<BM, BN, NW, BK, NST>::NS;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -479,7 +481,7 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
     // the step that K ends inside, or an empty one that makes up a pair: bytes past K are zeros
     auto load_tail = [&](int s, uint8_t *buf) __attribute__((always_inline)) {
         const int k = s * BK + chunk0 * 16;
-        constexpr int G = (LX + LW) % 4 == 0 ? 4 : 2;
+        constexpr int G = (LX + LW) % 4 == 0 ? 4 : (LX + LW) % 2 == 0 ? 2 : 1;
 #pragma unroll
         for (int j = 0; j < LX + LW; j += G) {
             i4 v[G];
@@ -646,7 +648,7 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
     // A lane holds token lane % 32 of a block and channels 8 g + 4 (lane / 32) + 0 .. 3.  32 tokens at a
     // time go through LDS (16-byte chunk c of row r at c ^ r) and come back as rows, eight channels a lane,
     // in a loop: unrolled, this code is so long that fetching it takes longer than running it.
-    constexpr int CW = KW ? BN : BN / 2, CHUNKS = CW / 4;   // channels of a wave, their chunks in a row
+    constexpr int CW = BN / WC, CHUNKS = CW / 4;   // channels of a wave, their chunks in a row
     constexpr int REGION = 32 * CW * 4;
     static_assert(NW * REGION * (KW ? TT : 1) <= NST * STAGE, "the waves' rows fit");
     const int c8 = lane % (CW / 8) * 8, n = wc * CW + c8;
@@ -721,14 +723,13 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
     }
 }
 
-template <int BM, int BN, int NW, W8Mode MODE>
+template <int BM, int BN, int NW, int BK, int NST, W8Mode MODE>
 __global__ __launch_bounds__(NW * 64, 1)
 void w8a8_tile_kernel(W8Args p)
 {
-    __shared__ W8Shared<BM, BN, NW> sh;
+    __shared__ W8Shared<BM, BN, NW, BK, NST> sh;
     W8Tile t;
     // K in steps of BK bytes, in pairs; tiles of 64 take its end on their own
-    constexpr int BK = 32 * NW;
     const int full = p.K / BK, steps = BM * BN == 64 * 64 || full * BK == p.K ? full : full + 1;
     int s0 = 0, s1 = (steps + 1) / 2 * 2, split = 0;
     if constexpr (MODE == EXPERTS) {
@@ -759,10 +760,10 @@ void w8a8_tile_kernel(W8Args p)
     // without; 256 rows 217 and 235, 221 and 249).
     if constexpr (MODE == EXPERTS && BM > 64)
         if (t.last - t.first <= BM / 2) {
-            w8a8_tile<BM / 2, BN, NW, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
+            w8a8_tile<BM / 2, BN, NW, BK, NST, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
             return;
         }
-    w8a8_tile<BM, BN, NW, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
+    w8a8_tile<BM, BN, NW, BK, NST, MODE>(p, t, s0, s1, split, sh.stages, sh.sc);
 }
 
 // Sums of the splits' planes, in their order, scaled and rounded: four channels of a row a thread
@@ -846,67 +847,75 @@ void stream_experts(const W8Args &a, hipStream_t s)
     w8a8_stream_experts_kernel<CH, WV, NST><<<dim3((a.N + CH - 1) / CH, a.E + more), WV * 64, 0, s>>>(a);
 }
 
-template <int B, int NW, W8Mode MODE>
+template <int BM, int BN, int NW, int BK, int NST, W8Mode MODE>
 void tile_launch(const W8Args &a, int64_t tiles, hipStream_t s)
 {
-    w8a8_tile_kernel<B, B, NW, MODE><<<(unsigned)round_up(tiles, 8), NW * 64, 0, s>>>(a);
+    w8a8_tile_kernel<BM, BN, NW, BK, NST, MODE><<<(unsigned)round_up(tiles, 8), NW * 64, 0, s>>>(a);
+}
+
+// Tiles of rows x channels and the estimated time (us) of a launch of them: a
+// start and an end, then per 128 bytes of K a time for each tile a CU has to
+// take and one for the tile's own start and end; or, where a CU has no more than
+// one, a time for K alone.  The constants are fitted to the choice among 3100
+// launches (195 shapes of 371 to 28672 channels, K 192 to 14336 and 69 to 4096
+// rows, unsplit and split; 30 by expert): it takes 0.6 % longer than the best of
+// them on average, 21 % at most.
+struct W8Cost {
+    int rows, channels;
+    double ends, step, tile, alone;
+};
+constexpr W8Cost kCosts[] = {{64, 64, 3.85, 0.213, 0.51, 0.151},
+                             {128, 128, 4.2, 0.516, 0.65, 0.769},
+                             {128, 256, 5.57, 0.796, 2.63, 0.725},
+                             {256, 256, 14.6, 1.286, 5.29, 1.102}};
+constexpr int kSizes = sizeof(kCosts) / sizeof(kCosts[0]);
+
+double tiles_time(const W8Cost &c, int64_t tiles, int pairs)
+{
+    const int64_t each = (tiles + kCUs - 1) / kCUs;
+    return c.ends + (each > 1 ? each * (pairs * 2 * c.step + c.tile) : pairs * 2 * c.alone);
 }
 
 template <W8Mode MODE>
 void tile_launch(const W8Args &a, int size, int64_t tiles, hipStream_t s)
 {
-    if (size == 64 && tiles <= kCUs)
-        tile_launch<64, 8, MODE>(a, tiles, s);
-    else if (size == 64)
-        tile_launch<64, 4, MODE>(a, tiles, s);
-    else if (size == 128)
-        tile_launch<128, 4, MODE>(a, tiles, s);
+    if (size == 0 && tiles <= kCUs)
+        tile_launch<64, 64, 8, 256, 4, MODE>(a, tiles, s);
+    else if (size == 0)
+        tile_launch<64, 64, 4, 128, 4, MODE>(a, tiles, s);
+    else if (size == 1)
+        tile_launch<128, 128, 4, 128, 2, MODE>(a, tiles, s);
+    else if (size == 2)
+        tile_launch<128, 256, 8, 128, 3, MODE>(a, tiles, s);
     else
-        tile_launch<256, 4, MODE>(a, tiles, s);
+        tile_launch<256, 256, 4, 128, 2, MODE>(a, tiles, s);
 }
 
 struct W8Plan {
-    int size, splits;                                 // tile, workgroups that share K
+    int size, splits;                                 // of kCosts; workgroups that share K
     int64_t tiles;
 };
 
 // workgroups of one launch: a grid holds fewer than 2^32 threads
 constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 
-// Estimated time (us) of a launch of tiles: a start and an end, then per 128
-// bytes of K a time for each tile a CU has to take, another one where it has no
-// more than one.  The constants are fitted to the choice among 2300 measured
-// launches (195 shapes of 371 to 28672 channels, K 192 to 14336 and 69 to 4096
-// rows; each tile size unsplit and split): it takes 0.3 % longer than the best
-// of them on average and 19 % at most.
-struct W8Cost {
-    int size;
-    double ends, step, alone;
-};
-constexpr W8Cost kCosts[] = {{64, 4.7, 0.28, 0.12}, {128, 4.4, 0.55, 0.87}, {256, 17.2, 1.68, 1.14}};
-
-double tiles_time(const W8Cost &c, int64_t tiles, int pairs)
-{
-    const int64_t each = (tiles + kCUs - 1) / kCUs;
-    return c.ends + pairs * 2 * (each > 1 ? each * c.step : c.alone);
-}
-
 // The tile size and split with the least estimated time.  A split adds the pass
 // over the partial sums.
 W8Plan w8_plan(int rows, int N, int K)
 {
     const int pairs = (K + 255) / 256;
-    W8Plan best = {64, 1, 0};
+    W8Plan best = {0, 1, 0};
     double time = -1.0;
-    for (const W8Cost &c : kCosts) {
-        const int64_t tiles = (((int64_t)rows + c.size - 1) / c.size) * (((int64_t)N + c.size - 1) / c.size);
-        if (tiles >= kMaxTiles && c.size < 256) continue;
+    for (int i = 0; i < kSizes; ++i) {
+        const W8Cost &c = kCosts[i];
+        const int64_t tiles = (((int64_t)rows + c.rows - 1) / c.rows) * (((int64_t)N + c.channels - 1) / c.channels);
+        if (tiles >= kMaxTiles && i + 1 < kSizes) continue;
         for (int splits = 1; splits <= 8 && (splits == 1 || splits * 2 <= pairs); splits *= 2) {
-            const double reduce = splits > 1 ? 2.4 + (double)splits * rows * N * 8 / 4.2e6 : 0.0;
+            const double reduce = splits > 1 ? 3.5 + (double)splits * rows * N * 8 / 5.8e6 : 0.0;
             const double us = tiles_time(c, tiles * splits, (pairs + splits - 1) / splits) + reduce;
             if (time < 0.0 || us < time) {
                 time = us;
-                best = {c.size, splits, tiles * splits};
+                best = {i, splits, tiles * splits};
             }
         }
     }
@@ -955,9 +964,10 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 //                               tiles of 64  56       76       79       81       84
 //   8 experts of 4096 x 4096:   stream       16       27       28       30       35
 //                               tiles of 64  17       32       32       32       32
-//   rows an expert                           64                 256
-//   128 experts: tiles of 64 / 128 / 256     108 /  93 / 110    257 / 176 / 182
-//   8 experts                                 39 /  38 /  48     78 /  74 /  61
+//   rows an expert                           64                       256
+//   128 experts: tiles of 64 / 128 / 128 x 256 / 256
+//                                           108 / 93 /  90 / 104     257 / 204 / 201 / 216
+//   8 experts                                39 / 35 /  31 /  46      78 /  72 /  67 /  62
 // All 1536 rows of 128 experts with one of them: 50 (tiles of 64: 16).
 // A ring of four waves and three stages holds twelve units of K: with fewer of
 // them two waves and two stages serve more workgroups a CU (128 experts of
@@ -976,19 +986,21 @@ hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
     }
     // the size whose tiles take the least estimated time, an expert's last tile being half full and every expert
     // having a row; at most one more tile for each of them is launched
-    int size = 0;
+    int size = -1;
+    int64_t most = 0;
     double time = 0.0;
-    auto tiles = [&](int size) { return ((int64_t)a.rows / size + a.E) * (((int64_t)a.N + size - 1) / size); };
-    for (const W8Cost &c : kCosts) {
-        if (tiles(c.size) >= kMaxTiles && c.size < 256) continue;
-        const int64_t likely = std::max((int64_t)a.E, (int64_t)a.rows / c.size + a.E / 2);
-        const double us = tiles_time(c, likely * ((a.N + c.size - 1) / c.size), (a.K + 255) / 256);
-        if (size == 0 || us < time) {
+    for (int i = 0; i < kSizes; ++i) {
+        const W8Cost &c = kCosts[i];
+        const int64_t nt = ((int64_t)a.N + c.channels - 1) / c.channels, whole = (int64_t)a.rows / c.rows;
+        if ((whole + a.E) * nt >= kMaxTiles && i + 1 < kSizes) continue;
+        const double us = tiles_time(c, std::max((int64_t)a.E, whole + a.E / 2) * nt, (a.K + 255) / 256);
+        if (size < 0 || us < time) {
+            size = i;
+            most = (whole + a.E) * nt;
             time = us;
-            size = c.size;
         }
     }
-    tile_launch<EXPERTS>(a, size, tiles(size), s);
+    tile_launch<EXPERTS>(a, size, most, s);
     return hipGetLastError();
 }
 
