@@ -85,9 +85,11 @@ def test_gemm_parity(M, N, K, dt, bias):
 
 @pytest.mark.parametrize("M,N,K", [
     (4090, 4095, 8200), (4096, 4096, 4096), (700, 9000, 520),
-    # tiles of 64 (more than one a CU), 128, 256; K shared by 2, 4 and 8 workgroups in tiles of 64, 128 and 256
+    # tiles of 64 (more than one a CU), 128, 256; K shared by workgroups
     (150, 6001, 200), (70, 9001, 208), (1500, 1502, 200), (3000, 4097, 2056), (24, 20567, 20384), (1500, 1501, 8200),
     (70, 9001, 4104), (70, 9002, 14328), (1001, 4097, 8200), (150, 9001, 14328),
+    # 128 x 256 unsplit and by 2 and 4; 128 by 4; 256 by 2 and 4
+    (1001, 4097, 200), (333, 6003, 8200), (150, 6001, 8200), (2100, 777, 14328), (131, 16463, 16184), (8193, 133, 18136),
 ])
 def test_gemm_large(M, N, K):
     """Sizes of the wider tiles, ragged and not; the 64-bit product on the GPU, all values."""
@@ -284,6 +286,8 @@ def test_experts_uneven(E, counts, N, K, gather):
     ({0: 1000, 5: 2064, 14: 1896, 15: 40}, 16, 333, 136),
     ({0: 2300, 1: 1412, 2: 1288}, 3, 3001, 2056), ({0: 128, 1: 2432, 2: 2440}, 3, 3001, 2064),  # of 256
     ({e: 20 + e for e in range(0, 40)}, 40, 333, 136),                                         # of 64
+    ({0: 128, 2: 129, 3: 640, 9: 65, 12: 64, 13: 192, 14: 500, 15: 282}, 16, 1500, 136),       # of 128 x 256
+    ({0: 300, 4: 1000, 15: 700}, 16, 2001, 2088),
 ])
 @pytest.mark.parametrize("gather,dt", [(True, "bf16"), (False, "f16")])
 def test_experts_large(counts, E, N, K, gather, dt):
