@@ -288,6 +288,9 @@ def test_experts_uneven(E, counts, N, K, gather):
     ({e: 20 + e for e in range(0, 40)}, 40, 333, 136),                                         # of 64
     ({0: 128, 2: 129, 3: 640, 9: 65, 12: 64, 13: 192, 14: 500, 15: 282}, 16, 1500, 136),       # of 128 x 256
     ({0: 300, 4: 1000, 15: 700}, 16, 2001, 2088),
+    # one to sixteen experts a lane of the tile search, some of them empty
+    ({e: e % 29 + 1 for e in range(0, 256, 1)}, 256, 40, 72), ({e: e % 31 for e in range(1, 257)}, 257, 70, 64),
+    ({e: e % 27 + 2 for e in range(0, 1024)}, 1024, 33, 72), ({1: 1, 700: 13000, 1023: 70}, 1024, 64, 128),
 ])
 @pytest.mark.parametrize("gather,dt", [(True, "bf16"), (False, "f16")])
 def test_experts_large(counts, E, N, K, gather, dt):
