@@ -25,7 +25,6 @@ namespace {
 
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
-typedef int i4a __attribute__((ext_vector_type(4), aligned(8)));   // rows start at multiples of 8 bytes
 
 __device__ __forceinline__ void put(void *y, int64_t o, float v, int bf16)
 {
