@@ -810,14 +810,6 @@ namespace {
 
 constexpr int kCUs = 256;
 
-// A dense product streams the weights where one pass over them serves all rows
-// faster than tiles do: up to 16 rows, and up to 64 where a wave of workgroups
-// takes at most 32 channels each (w8a8_stream_rows has the figures).
-bool w8_streams(int rows, int N)
-{
-    return rows <= 16 || (rows <= 64 && N <= 32 * kCUs);
-}
-
 template <int CH, int WV, int NST, int XL>
 void stream(const W8Args &a, hipStream_t s)
 {
@@ -893,6 +885,7 @@ void tile_launch(const W8Args &a, int size, int64_t tiles, hipStream_t s)
 struct W8Plan {
     int size, splits;                                 // of kCosts; workgroups that share K
     int64_t tiles;
+    double time;
 };
 
 // workgroups of one launch: a grid holds fewer than 2^32 threads
@@ -903,8 +896,7 @@ constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 W8Plan w8_plan(int rows, int N, int K)
 {
     const int pairs = (K + 255) / 256;
-    W8Plan best = {0, 1, 0};
-    double time = -1.0;
+    W8Plan best = {0, 1, 0, -1.0};
     for (int i = 0; i < kSizes; ++i) {
         const W8Cost &c = kCosts[i];
         const int64_t tiles = (((int64_t)rows + c.rows - 1) / c.rows) * (((int64_t)N + c.channels - 1) / c.channels);
@@ -912,20 +904,33 @@ W8Plan w8_plan(int rows, int N, int K)
         for (int splits = 1; splits <= 8 && (splits == 1 || splits * 2 <= pairs); splits *= 2) {
             const double reduce = splits > 1 ? 3.5 + (double)splits * rows * N * 8 / 5.8e6 : 0.0;
             const double us = tiles_time(c, tiles * splits, (pairs + splits - 1) / splits) + reduce;
-            if (time < 0.0 || us < time) {
-                time = us;
-                best = {i, splits, tiles * splits};
-            }
+            if (best.time < 0.0 || us < best.time) best = {i, splits, tiles * splits, us};
         }
     }
     return best;
+}
+
+// A dense product streams the weights where one pass over them serves all rows
+// faster than tiles do: up to 16 rows, and up to 64 by an estimate: a start and
+// an end, then what a workgroup brings to its CU (faster where half of them have
+// none) or the weights from memory.  Measured on 120 shapes of 24 to 64 rows, 200
+// to 8192 channels, K 2048 to 28672, this takes 0.3 % longer than the better of
+// both on average, 12 % at most (64 x 4096: K = 4096 7.2 us against 9.3 in tiles,
+// K = 12432 19.7 against 15.8).
+bool w8_streams(int rows, int N, int K)
+{
+    if (rows <= 16) return true;
+    if (rows > 64 || N > 32 * kCUs) return false;
+    const int channels = N <= 16 * kCUs ? 16 : 32, workgroups = (N + channels - 1) / channels;
+    const double own = (double)K * (channels + (rows <= 32 ? 32 : 64)) / (workgroups > kCUs / 2 ? 72e3 : 90e3);
+    return 2.0 + std::max(own, (double)N * K / 5e6) <= 1.1 * w8_plan(rows, N, K).time;
 }
 
 }  // namespace
 
 size_t gemm_w8a8_workspace(int M, int N, int K)
 {
-    if (w8_streams(M, N)) return 0;
+    if (w8_streams(M, N, K)) return 0;
     const W8Plan pl = w8_plan(M, N, K);
     return pl.splits > 1 ? (size_t)pl.splits * M * N * sizeof(int32_t) : 0;
 }
@@ -933,7 +938,7 @@ size_t gemm_w8a8_workspace(int M, int N, int K)
 hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 {
     W8Args a = args;
-    if (w8_streams(a.rows, a.N)) {
+    if (w8_streams(a.rows, a.N, a.K)) {
         if (a.rows <= 8)
             stream<1>(a, s);
         else if (a.rows <= 16)
