@@ -266,6 +266,33 @@ def test_rows_past_2_31_bytes():
 
 
 # ---------------------------------------------------------------- graphs
+def test_most_tokens():
+    """2^24 - 1 tokens, the most there may be: the index against torch's stable sort, rows and sums exact."""
+    T, H, E = (1 << 24) - 1, 8, 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(0, E, (T, 1), dtype=torch.int32, device="cuda", generator=g)
+    nb = lb.lowbit_moe_sort_workspace_bytes(T, 1, E)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    rs, sr = (torch.full((T,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    of = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    lb.check(lb.lowbit_moe_sort(ids, T, 1, E, None, E, rs, sr, of, ws, nb))
+    order = torch.sort(ids.view(-1), stable=True).indices
+    assert torch.equal(rs.long(), order)
+    assert torch.equal(sr[order].long(), torch.arange(T, device="cuda"))
+    assert of.tolist() == [0] + torch.cumsum(torch.bincount(ids.view(-1).long(), minlength=E), 0).tolist()
+    x = torch.randint(-8, 9, (T, H), device="cuda", generator=g).half()
+    w = torch.randint(-4, 5, (T, 1), device="cuda", generator=g).float()
+    xp, y, dyp = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
+    dw = torch.zeros((T, 1), device="cuda")
+    lb.check(lb.lowbit_moe_permute(x, None, T, 1, 2 * H, sr, xp, None))
+    assert torch.equal(xp, x[order])
+    lb.check(lb.lowbit_moe_unpermute(xp, lb.LOWBIT_F16, w, T, 1, H, sr, y))
+    assert torch.equal(y, (w * x.float()).half())
+    lb.check(lb.lowbit_moe_unpermute_backward(x, xp, lb.LOWBIT_F16, w, T, 1, H, sr, dyp, dw))
+    assert torch.equal(dyp, (w * x.float()).half()[order])
+    assert torch.equal(dw.view(-1), (x.float() * x.float()).sum(1))
+
+
 @pytest.mark.parametrize("T", [40, 3000])
 def test_sort_and_rows_graph_replays(T):
     """Sort, permute, unpermute and its gradient captured once and replayed on new routings."""

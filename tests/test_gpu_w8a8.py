@@ -122,6 +122,21 @@ def test_gemm_largest_sums_are_exact(M):
     assert_rounded(y, y64, step, torch.bfloat16)
 
 
+@pytest.mark.parametrize("M,N", [((1 << 24) - 1, 3), (2, (1 << 24) - 1), (70, (1 << 24) - 1)])
+def test_gemm_most_rows_and_channels(M, N):
+    """2^24 - 1 rows or channels, the most there may be; sums of small codes, exact in the output type."""
+    K = 8
+    g = torch.Generator(device="cuda").manual_seed(M % 1000)
+    xq = torch.randint(-3, 4, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    wq = torch.randint(-3, 4, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    y = gemm(xq, torch.ones(M, device="cuda"), wq, torch.ones(N, device="cuda"), None, "f16")
+    step = 1 << 20
+    for lo in range(0, max(M, N), step):
+        a, b = (xq[lo:lo + step], wq) if M > N else (xq, wq[lo:lo + step])
+        want = a.float() @ b.float().t()
+        assert torch.equal((y[lo:lo + step] if M > N else y[:, lo:lo + step]).float(), want)
+
+
 def test_gemm_one_hot_is_exact():
     """One code 1 per token and scales of 1 return the weights' codes themselves."""
     rng = np.random.default_rng(11)
