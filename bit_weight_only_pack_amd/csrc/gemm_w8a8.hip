@@ -816,14 +816,31 @@ void stream(const W8Args &a, hipStream_t s)
     w8a8_stream_kernel<CH, WV, NST, XL><<<(a.N + CH - 1) / CH, WV * 64, 0, s>>>(a);
 }
 
+// The kernel a product takes: streaming, or tiles of rows x channels with K
+// split over `splits` workgroups.
+struct W8Choice {
+    bool stream;
+    int rows, channels, waves;                        // of a workgroup
+    int splits;
+    int64_t tiles;                                    // workgroups of the tile kernel (by expert: at most)
+};
+
 // As few channels a workgroup as give every CU one, as many rows as there are.
+W8Choice stream_choice(int rows, int N)
+{
+    const int up_to = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    if (N <= 16 * kCUs) return {true, up_to, 16, 8, 1, 0};
+    if (up_to > 16 || N <= 32 * kCUs) return {true, up_to, 32, up_to == 64 ? 4 : 8, 1, 0};
+    return {true, up_to, 64, 4, 1, 0};
+}
+
 template <int XL>
-void stream(const W8Args &a, hipStream_t s)
+void stream(const W8Args &a, const W8Choice &c, hipStream_t s)
 {
     constexpr bool kMany = XL == 8;                   // the rings of 64 rows leave room for less
-    if (a.N <= 16 * kCUs)
+    if (c.channels == 16)
         stream<16, 8, kMany ? 2 : 3, XL>(a, s);
-    else if (XL > 2 || a.N <= 32 * kCUs)
+    else if (XL > 2 || c.channels == 32)
         stream<32, kMany ? 4 : 8, 2, XL>(a, s);
     else if constexpr (XL <= 2)
         stream<64, 4, 2, XL>(a, s);
@@ -867,19 +884,27 @@ double tiles_time(const W8Cost &c, int64_t tiles, int pairs)
     return c.ends + (each > 1 ? each * (pairs * 2 * c.step + c.tile) : pairs * 2 * c.alone);
 }
 
-template <W8Mode MODE>
-void tile_launch(const W8Args &a, int size, int64_t tiles, hipStream_t s)
+// Tiles of 64 x 64 share K among eight waves where a CU has no more than one of them.
+W8Choice tile_choice(int size, int splits, int64_t tiles)
 {
-    if (size == 0 && tiles <= kCUs)
-        tile_launch<64, 64, 8, 256, 4, MODE>(a, tiles, s);
-    else if (size == 0)
-        tile_launch<64, 64, 4, 128, 4, MODE>(a, tiles, s);
-    else if (size == 1)
-        tile_launch<128, 128, 4, 128, 2, MODE>(a, tiles, s);
-    else if (size == 2)
-        tile_launch<128, 256, 8, 128, 3, MODE>(a, tiles, s);
+    const W8Cost &c = kCosts[size];
+    const bool eight = c.rows == 64 ? tiles <= kCUs : c.rows != c.channels;
+    return {false, c.rows, c.channels, eight ? 8 : 4, splits, tiles};
+}
+
+template <W8Mode MODE>
+void tile_launch(const W8Args &a, const W8Choice &c, hipStream_t s)
+{
+    if (c.rows == 64 && c.waves == 8)
+        tile_launch<64, 64, 8, 256, 4, MODE>(a, c.tiles, s);
+    else if (c.rows == 64)
+        tile_launch<64, 64, 4, 128, 4, MODE>(a, c.tiles, s);
+    else if (c.channels == 128)
+        tile_launch<128, 128, 4, 128, 2, MODE>(a, c.tiles, s);
+    else if (c.rows == 128)
+        tile_launch<128, 256, 8, 128, 3, MODE>(a, c.tiles, s);
     else
-        tile_launch<256, 256, 4, 128, 2, MODE>(a, tiles, s);
+        tile_launch<256, 256, 4, 128, 2, MODE>(a, c.tiles, s);
 }
 
 struct W8Plan {
@@ -926,37 +951,43 @@ bool w8_streams(int rows, int N, int K)
     return 2.0 + std::max(own, (double)N * K / 5e6) <= 1.1 * w8_plan(rows, N, K).time;
 }
 
+W8Choice dense_choice(int rows, int N, int K)
+{
+    if (w8_streams(rows, N, K)) return stream_choice(rows, N);
+    const W8Plan pl = w8_plan(rows, N, K);
+    return tile_choice(pl.size, pl.splits, pl.tiles);
+}
+
 }  // namespace
 
 size_t gemm_w8a8_workspace(int M, int N, int K)
 {
-    if (w8_streams(M, N, K)) return 0;
-    const W8Plan pl = w8_plan(M, N, K);
-    return pl.splits > 1 ? (size_t)pl.splits * M * N * sizeof(int32_t) : 0;
+    const W8Choice c = dense_choice(M, N, K);
+    return c.splits > 1 ? (size_t)c.splits * M * N * sizeof(int32_t) : 0;
 }
 
 hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 {
     W8Args a = args;
-    if (w8_streams(a.rows, a.N, a.K)) {
-        if (a.rows <= 8)
-            stream<1>(a, s);
-        else if (a.rows <= 16)
-            stream<2>(a, s);
-        else if (a.rows <= 32)
-            stream<4>(a, s);
+    const W8Choice c = dense_choice(a.rows, a.N, a.K);
+    if (c.stream) {
+        if (c.rows == 8)
+            stream<1>(a, c, s);
+        else if (c.rows == 16)
+            stream<2>(a, c, s);
+        else if (c.rows == 32)
+            stream<4>(a, c, s);
         else
-            stream<8>(a, s);
+            stream<8>(a, c, s);
         return hipGetLastError();
     }
-    const W8Plan pl = w8_plan(a.rows, a.N, a.K);
-    a.splits = pl.splits;
+    a.splits = c.splits;
     a.part = static_cast<int32_t *>(ws);
-    if (pl.splits > 1) {
-        tile_launch<SPLIT>(a, pl.size, pl.tiles, s);
+    if (c.splits > 1) {
+        tile_launch<SPLIT>(a, c, s);
         reduce_launch(a, s);
     } else {
-        tile_launch<DENSE>(a, pl.size, pl.tiles, s);
+        tile_launch<DENSE>(a, c, s);
     }
     return hipGetLastError();
 }
@@ -977,17 +1008,13 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 // them two waves and two stages serve more workgroups a CU (128 experts of
 // 2048 x 768, 1 / 4 / 8 rows each: 24 / 35 / 36 against 34 / 47 / 50; of
 // 1536 x 2048: 46 / 66 / 69 against 45 / 64 / 66).
-hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
+//
+// gathered: rows of x that row_slot picks from, 0 where rows lie in expert order
+static W8Choice experts_choice(int E, int rows, int N, int K, int64_t gathered)
 {
     // the rows' offsets inside x are 32-bit in the tile kernel when they are gathered
-    const bool far = a.row_slot != nullptr && (int64_t)a.x_rows * a.K >= ((int64_t)1 << 32);
-    if (a.rows <= 12 * a.E || far) {
-        if (a.K < 12 * 128)
-            stream_experts<32, 2, 2>(a, s);
-        else
-            stream_experts<32, 4, 3>(a, s);
-        return hipGetLastError();
-    }
+    const bool far = gathered * K >= (int64_t)1 << 32;
+    if (rows <= 12 * E || far) return {true, 16, 32, K < 12 * 128 ? 2 : 4, 1, 0};
     // the size whose tiles take the least estimated time, an expert's last tile being half full and every expert
     // having a row; at most one more tile for each of them is launched
     int size = -1;
@@ -995,17 +1022,35 @@ hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
     double time = 0.0;
     for (int i = 0; i < kSizes; ++i) {
         const W8Cost &c = kCosts[i];
-        const int64_t nt = ((int64_t)a.N + c.channels - 1) / c.channels, whole = (int64_t)a.rows / c.rows;
-        if ((whole + a.E) * nt >= kMaxTiles && i + 1 < kSizes) continue;
-        const double us = tiles_time(c, std::max((int64_t)a.E, whole + a.E / 2) * nt, (a.K + 255) / 256);
+        const int64_t nt = ((int64_t)N + c.channels - 1) / c.channels, whole = (int64_t)rows / c.rows;
+        if ((whole + E) * nt >= kMaxTiles && i + 1 < kSizes) continue;
+        const double us = tiles_time(c, std::max((int64_t)E, whole + E / 2) * nt, (K + 255) / 256);
         if (size < 0 || us < time) {
             size = i;
-            most = (whole + a.E) * nt;
+            most = (whole + E) * nt;
             time = us;
         }
     }
-    tile_launch<EXPERTS>(a, size, most, s);
+    return tile_choice(size, 1, most);
+}
+
+hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)
+{
+    const W8Choice c = experts_choice(a.E, a.rows, a.N, a.K, a.row_slot != nullptr ? a.x_rows : 0);
+    if (!c.stream)
+        tile_launch<EXPERTS>(a, c, s);
+    else if (c.waves == 2)
+        stream_experts<32, 2, 2>(a, s);
+    else
+        stream_experts<32, 4, 3>(a, s);
     return hipGetLastError();
 }
 
 }  // namespace lowbit
+
+void lowbit_internal_w8a8_choice(int E, int rows, int N, int K, int gathered, int *choice)
+{
+    const lowbit::W8Choice c = E > 0 ? lowbit::experts_choice(E, rows, N, K, gathered) : lowbit::dense_choice(rows, N, K);
+    const int of[] = {c.stream, c.rows, c.channels, c.waves, c.splits};
+    std::copy(of, of + 5, choice);
+}

@@ -41,3 +41,10 @@ hipError_t launch_moe_unpermute_backward(const void *dy, const void *yp, int bf1
                                          int H, const int32_t *slot_row, void *dyp, float *dw, hipStream_t s);
 
 }  // namespace lowbit
+
+// Not part of the library's interface: the kernel that a product of these sizes
+// (as the entry points accept them) takes, so that a test can name the one it is
+// for.  E = 0: dense; gathered: rows of x that row_slot picks from, 0 without it.
+// choice: streaming or tiles (1 / 0), rows, channels and waves of a workgroup,
+// workgroups that share K.
+extern "C" void lowbit_internal_w8a8_choice(int E, int rows, int N, int K, int gathered, int *choice);
