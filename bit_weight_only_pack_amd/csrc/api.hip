@@ -735,7 +735,7 @@ int check_slots(int T, int top_k)
 
 size_t lowbit_gemm_w8a8_workspace_bytes(int M, int N, int K)
 {
-    if (check_w8_shape(M, N, K) != LOWBIT_OK || M == 0 || N == 0) return 0;
+    if (check_w8_shape(M, N, K) != LOWBIT_OK || !gemm_w8a8_fits(M, N) || M == 0 || N == 0) return 0;
     return gemm_w8a8_workspace(M, N, K);
 }
 
@@ -745,7 +745,7 @@ int lowbit_gemm_w8a8(int M, int N, int K, const int8_t *xq, const float *x_scale
 {
     const int st = check_w8_shape(M, N, K);
     if (st != LOWBIT_OK) return st;
-    if (y_dtype != LOWBIT_F16 && y_dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+    if (!gemm_w8a8_fits(M, N) || (y_dtype != LOWBIT_F16 && y_dtype != LOWBIT_BF16)) return LOWBIT_E_UNSUPPORTED;
     if (M == 0 || N == 0) return LOWBIT_OK;
     if (x_scale == nullptr || w_scale == nullptr || y == nullptr || (K > 0 && (xq == nullptr || wq == nullptr)))
         return LOWBIT_E_INVALID_ARG;

@@ -913,20 +913,29 @@ struct W8Plan {
     double time;
 };
 
-// workgroups of one launch: a grid holds fewer than 2^32 threads
-constexpr int64_t kMaxTiles = (int64_t)1 << 23;
+// One launch has that many tiles: a grid holds fewer than 2^32 threads.
+bool grid_holds(const W8Cost &c, int64_t tiles)
+{
+    const int64_t threads = c.rows != c.channels ? 512 : 256;      // the tiles of 64 take 512 only where they are few
+    return (int64_t)round_up(tiles, 8) * threads < (int64_t)1 << 32;
+}
 
-// The tile size and split with the least estimated time.  A split adds the pass
-// over the partial sums.
+int64_t tiles_of(const W8Cost &c, int rows, int N)
+{
+    return (((int64_t)rows + c.rows - 1) / c.rows) * (((int64_t)N + c.channels - 1) / c.channels);
+}
+
+// The tile size and split with the least estimated time, of those that a grid
+// holds.  A split adds the pass over the partial sums.
 W8Plan w8_plan(int rows, int N, int K)
 {
     const int pairs = (K + 255) / 256;
     W8Plan best = {0, 1, 0, -1.0};
     for (int i = 0; i < kSizes; ++i) {
         const W8Cost &c = kCosts[i];
-        const int64_t tiles = (((int64_t)rows + c.rows - 1) / c.rows) * (((int64_t)N + c.channels - 1) / c.channels);
-        if (tiles >= kMaxTiles && i + 1 < kSizes) continue;
+        const int64_t tiles = tiles_of(c, rows, N);
         for (int splits = 1; splits <= 8 && (splits == 1 || splits * 2 <= pairs); splits *= 2) {
+            if (!grid_holds(c, tiles * splits)) break;
             const double reduce = splits > 1 ? 3.5 + (double)splits * rows * N * 8 / 5.8e6 : 0.0;
             const double us = tiles_time(c, tiles * splits, (pairs + splits - 1) / splits) + reduce;
             if (best.time < 0.0 || us < best.time) best = {i, splits, tiles * splits, us};
@@ -959,6 +968,12 @@ W8Choice dense_choice(int rows, int N, int K)
 }
 
 }  // namespace
+
+bool gemm_w8a8_fits(int M, int N)
+{
+    const W8Cost &most = kCosts[kSizes - 1];
+    return M <= 16 || grid_holds(most, tiles_of(most, M, N));
+}
 
 size_t gemm_w8a8_workspace(int M, int N, int K)
 {
@@ -1014,16 +1029,18 @@ static W8Choice experts_choice(int E, int rows, int N, int K, int64_t gathered)
 {
     // the rows' offsets inside x are 32-bit in the tile kernel when they are gathered
     const bool far = gathered * K >= (int64_t)1 << 32;
-    if (rows <= 12 * E || far) return {true, 16, 32, K < 12 * 128 ? 2 : 4, 1, 0};
+    const W8Choice few = {true, 16, 32, K < 12 * 128 ? 2 : 4, 1, 0};
+    if (rows <= 12 * E || far) return few;
     // the size whose tiles take the least estimated time, an expert's last tile being half full and every expert
-    // having a row; at most one more tile for each of them is launched
+    // having a row; at most one more tile for each of them is launched.  Where no grid holds them (many experts of
+    // millions of channels) the streaming kernel goes on: its runs of rows are shared by as many workgroups as there are
     int size = -1;
     int64_t most = 0;
     double time = 0.0;
     for (int i = 0; i < kSizes; ++i) {
         const W8Cost &c = kCosts[i];
         const int64_t nt = ((int64_t)N + c.channels - 1) / c.channels, whole = (int64_t)rows / c.rows;
-        if ((whole + E) * nt >= kMaxTiles && i + 1 < kSizes) continue;
+        if (!grid_holds(c, (whole + E) * nt)) continue;
         const double us = tiles_time(c, std::max((int64_t)E, whole + E / 2) * nt, (K + 255) / 256);
         if (size < 0 || us < time) {
             size = i;
@@ -1031,7 +1048,7 @@ static W8Choice experts_choice(int E, int rows, int N, int K, int64_t gathered)
             time = us;
         }
     }
-    return tile_choice(size, 1, most);
+    return size < 0 ? few : tile_choice(size, 1, most);
 }
 
 hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s)

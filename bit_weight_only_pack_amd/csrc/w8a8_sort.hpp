@@ -25,6 +25,8 @@ __device__ __forceinline__ int w8a8_source_row(const W8Args &p, int r)
     if (p.row_slot == nullptr) return r;
     return min(max(p.row_slot[r], 0) / p.row_div, p.x_rows - 1);
 }
+// false: more tiles than a launch takes (2^40 outputs or so)
+bool gemm_w8a8_fits(int M, int N);
 size_t gemm_w8a8_workspace(int M, int N, int K);
 hipError_t launch_gemm_w8a8(const W8Args &a, void *ws, hipStream_t s);
 hipError_t launch_moe_gemm_w8a8(const W8Args &a, hipStream_t s);

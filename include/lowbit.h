@@ -286,8 +286,9 @@ int lowbit_gemv_w4a8_batched_noalloc(int fmt, int M, int group_size, int count, 
  * sum by x_scale, that by w_scale), and y is rounded to nearest even into
  * y_dtype.  Results do not depend on how the work is split: equal inputs give
  * equal bits.  One entry point for decode and prefill.
- *   M, N, K : any M and N below 2^24; K % 8 == 0 and K <= 131064 (the sum then
- *             fits int32 for codes -128..127), else LOWBIT_E_UNSUPPORTED
+ *   M, N, K : any M and N below 2^24 with at most 2^24 - 8 tiles of 256 x 256
+ *             outputs (M <= 16: any number); K % 8 == 0 and K <= 131064 (the sum
+ *             then fits int32 for codes -128..127), else LOWBIT_E_UNSUPPORTED
  *   xq      : i8  [M][K], 16-byte aligned; lowbit_quant_act_i8 makes it and x_scale
  *   x_scale : f32 [M]
  *   wq      : i8  [N][K], 16-byte aligned, read as it is (no packing)

@@ -58,3 +58,31 @@ def test_split_products_ask_for_a_workspace():
             call = lambda ws, n: lb.lowbit_gemm_w8a8(M, N, K, at, at, at, at, None, at, lb.LOWBIT_F16, ws, n)
             assert call(None, 0) == lb.LOWBIT_E_WORKSPACE and call(at, nb - 1) == lb.LOWBIT_E_WORKSPACE
             assert call(at + 128, nb) == lb.LOWBIT_E_INVALID_ARG
+
+
+def launch_fits(c, rows, N, E=0):
+    """The launch of this kernel has fewer than 2^32 threads along the grid's first side and 2^16 rows."""
+    up = lambda a, b: -(-a // b)
+    if c.stream:
+        more = min(rows // 16, max(8, min(rows // 128, 1 << 15))) if E else 0
+        return up(N, c.channels) * c.waves * 64 < 1 << 32 and E + more < 1 << 16
+    tiles = (rows // c.rows + E if E else up(rows, c.rows)) * up(N, c.channels) * c.splits
+    return up(tiles, 8) * 8 * c.waves * 64 < 1 << 32
+
+
+def test_launches_fit_a_grid():
+    """The largest sizes: a launch that a grid cannot hold is never chosen; what no kernel's grid holds is refused."""
+    big = (1 << 24) - 1
+    for M, N, K in ((big, 3, 8), (2, big, 8), (70, big, 8), (big, 256, 131064), (65536, 1 << 23, 64), (6016, big, 8)):
+        assert launch_fits(choice(M, N, K), M, N), (M, N, K)
+        assert lb.lowbit_gemm_w8a8_workspace_bytes(M, N, K) % (M * N * 4) == 0
+    for E, rows, N, K in ((256, 3073, big, 8), (1024, 12289, big, 8), (1000, 50000, 1 << 22, 16), (128, 1537, big, 8),
+                          (1, big, big, 64), (100, 4864, 60787 * 256, 8), (100, 4864, 60787 * 256, 1032),
+                          (512, 7000, 9 << 20, 2056), (1024, big, 4096, 4096), (3, 40, big, 8)):
+        for gathered in (0, 1000):
+            assert launch_fits(choice(rows, N, K, E, gathered), rows, N, E), (E, rows, N, K)
+    at = 1 << 20                                     # a non-null address that is not read on these paths
+    call = lambda M, N, K: lb.lowbit_gemm_w8a8(M, N, K, at, at, at, at, None, at, lb.LOWBIT_F16, at, 1 << 62)
+    for M, N in ((big, big), (big, 1 << 20), (1 << 20, 1 << 20), (1 << 23, 1 << 17)):     # 2^40 outputs and more
+        assert call(M, N, 8) == lb.LOWBIT_E_UNSUPPORTED, (M, N)
+        assert lb.lowbit_gemm_w8a8_workspace_bytes(M, N, 8) == 0
