@@ -338,7 +338,8 @@ typedef int i16v __attribute__((ext_vector_type(16)));
 
 // The tile of this workgroup among the tiles of all experts (their rows cut
 // into runs of BM): consecutive numbers go over an expert's row tiles first, so
-// that they share its weights.  False if there are fewer tiles.
+// that they share its weights.  False if there are fewer tiles, and for offsets
+// that overlap (row ranges of a table that does not ascend).
 struct W8Tile {
     int e, first, last, n0;
 };
@@ -363,7 +364,11 @@ __device__ __forceinline__ bool expert_tile(const W8Args &p, W8Tile &t)
         if (i > 0) mine += (max(at[i] - at[i - 1], 0) + BM - 1) / BM;
     }
     const int incl = wave_prefix_sum(mine);
-    const int total = __builtin_amdgcn_readlane(incl, 63) * nt;
+    // More than offsets that ascend can give: a damaged table, whose tiles times nt might pass 32 bits.  Up to here
+    // they are no more than were launched.
+    const int all = __builtin_amdgcn_readlane(incl, 63);
+    if (all > p.rows / BM + p.E) return false;
+    const int total = all * nt;
     const int run = (total + 7) / 8;                  // each XCD takes a run of tiles
     const int slot = blockIdx.x >> 3, lin = (blockIdx.x & 7) * run + slot;
     if (slot >= run || lin >= total) return false;

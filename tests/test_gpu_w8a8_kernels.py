@@ -111,3 +111,22 @@ def test_split_products_on_two_streams():
     torch.cuda.synchronize()
     for M, N, K, _, y, _, _, alone in sets:
         assert torch.equal(y.view(torch.int16), alone.view(torch.int16)), (M, N, K)
+
+
+@pytest.mark.parametrize("kernel,counts,sizes", EXPERTS, ids=lambda v: "x".join(map(str, v)) if len(v) < 6 else "")
+def test_experts_with_offsets_that_do_not_ascend(kernel, counts, sizes):
+    """Offsets that jump between both ends, whose row ranges overlap: what is computed is undefined, but every launch
+    ends and nothing beside the output is written."""
+    E, N, K = sizes
+    S = sum(counts.values())
+    assert choice(S, N, K, E) == kernel
+    g = torch.Generator(device="cuda").manual_seed(S)
+    xq, wq, xs, ws = codes(g, S, K), codes(g, E, N, K), scales(g, S), scales(g, E, N)
+    up_down = np.where(np.arange(E + 1) % 2 == 0, 0, S)
+    for offs in (up_down, S - up_down, np.linspace(S, 0, E + 1).astype(int),
+                 np.where(np.arange(E + 1) % 2 == 0, -2 ** 31, 2 ** 31 - 1)):
+        whole, y = guarded(S, N, torch.bfloat16)
+        lb.check(lb.lowbit_moe_gemm_w8a8(E, N, K, wq, ws, xq, xs, S, None, 1, dev(offs.astype(np.int32)), S, y,
+                                         lb.LOWBIT_BF16))
+        torch.cuda.synchronize()
+        assert guards_ok(whole)
