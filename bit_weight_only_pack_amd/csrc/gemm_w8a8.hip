@@ -6,9 +6,10 @@
 //
 // S is an exact int32 for every K the entry points accept (|xq wq| <= 2^14, so
 // K < 2^17), whatever the order of summation: splitting K over waves or
-// workgroups changes no bit of the result.  The scales are applied in fp32,
-// fl(fl(S * xs) * ws), S first so that two small scales cannot underflow
-// before S has lifted them; the one rounding to the output type is the last.
+// workgroups changes no bit of the result.  The scales and the bias are applied
+// in fp32, fl(fl(fl(S) * xs) * ws + bias) (`scaled` below, the one place that
+// does it), S first so that two small scales cannot underflow before S has
+// lifted them; the one rounding to the output type is the last.
 //
 // Both operands are row-major with K contiguous, which is the operand order of
 // v_mfma_i32_16x16x64_i8 (lane l: row l % 16, K bytes 16 (l / 16) .. + 15), so
@@ -25,6 +26,13 @@ namespace {
 
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
+
+// The product and the bias in one rounding, and said so: left to the compiler's contraction, kernels could differ in it.
+// Without a bias the sum is with zero, which rounds the product alone.
+__device__ __forceinline__ float scaled(int s, float xs, float ws, float bias)
+{
+    return __builtin_fmaf((float)s * xs, ws, bias);
+}
 
 __device__ __forceinline__ void put(void *y, int64_t o, float v, int bf16)
 {
@@ -251,7 +259,7 @@ __device__ __forceinline__ void w8a8_stream_rows(const W8Args &p, uint8_t *ring,
         int s = 0;
 #pragma unroll
         for (int q = 0; q < WV; ++q) s += part[q * 16 * TB * CH + i];
-        put(p.y, (int64_t)(first + m) * p.N + n0 + n, (float)s * xs[j] * wscale + bias, p.y_bf16);
+        put(p.y, (int64_t)(first + m) * p.N + n0 + n, scaled(s, xs[j], wscale, bias), p.y_bf16);
     }
 }
 
@@ -693,7 +701,7 @@ __device__ __forceinline__ void w8a8_tile(const W8Args &p, const W8Tile t, const
             const float xs = sc[tok];
             float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = (float)v[i / 4][i % 4] * xs * ws[i / 4][i % 4] + bs[i / 4][i % 4];
+            for (int i = 0; i < 8; ++i) f[i] = scaled(v[i / 4][i % 4], xs, ws[i / 4][i % 4], bs[i / 4][i % 4]);
             put8(p.y, o, f, n_valid - n, p.y_bf16);
         }
     };
@@ -784,7 +792,7 @@ __global__ __launch_bounds__(256) void w8a8_reduce_kernel(W8Args p)
         for (int q = 1; q < p.splits; ++q) s += *reinterpret_cast<const i4_any *>(p.part + q * MN + o);
         f4 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (float)s[j] * xs * p.ws[n + j] + (p.bias ? p.bias[n + j] : 0.f);
+        for (int j = 0; j < 4; ++j) v[j] = scaled(s[j], xs, p.ws[n + j], p.bias ? p.bias[n + j] : 0.f);
         if (p.y_bf16) {
             typedef __bf16 b4 __attribute__((ext_vector_type(4)));
             typedef b4 b4_any __attribute__((aligned(2)));
@@ -799,7 +807,7 @@ __global__ __launch_bounds__(256) void w8a8_reduce_kernel(W8Args p)
     for (int j = 0; n + j < p.N; ++j) {
         int s = p.part[o + j];
         for (int q = 1; q < p.splits; ++q) s += p.part[q * MN + o + j];
-        put(p.y, o + j, (float)s * xs * p.ws[n + j] + (p.bias ? p.bias[n + j] : 0.f), p.y_bf16);
+        put(p.y, o + j, scaled(s, xs, p.ws[n + j], p.bias ? p.bias[n + j] : 0.f), p.y_bf16);
     }
 }
 

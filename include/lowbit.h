@@ -282,10 +282,11 @@ int lowbit_gemv_w4a8_batched_noalloc(int fmt, int M, int group_size, int count, 
  * matrix-multiply instructions with int32 accumulation; the page names the
  * scheme, the definition below is this library's):
  *   y[m][n] = x_scale[m] * w_scale[n] * sum_k xq[m][k] * wq[n][k]  (+ bias[n])
- * The sum is an exact int32; the scales and the bias are applied in fp32 (the
- * sum by x_scale, that by w_scale), and y is rounded to nearest even into
- * y_dtype.  Results do not depend on how the work is split: equal inputs give
- * equal bits.  One entry point for decode and prefill.
+ * The sum is an exact int32; the scales and the bias are applied in fp32, p =
+ * fl(fl(sum) * x_scale), then fl(p * w_scale + bias) in one rounding (without a
+ * bias, + 0), and y is rounded to nearest even into y_dtype.  Results do not
+ * depend on how the work is split or on M: equal inputs give equal bits.  One
+ * entry point for decode and prefill.
  *   M, N, K : any M and N below 2^24 with at most 2^24 - 8 tiles of 256 x 256
  *             outputs (M <= 16: any number); K % 8 == 0 and K <= 131064 (the sum
  *             then fits int32 for codes -128..127), else LOWBIT_E_UNSUPPORTED

@@ -130,3 +130,74 @@ def test_experts_with_offsets_that_do_not_ascend(kernel, counts, sizes):
                                          lb.LOWBIT_BF16))
         torch.cuda.synchronize()
         assert guards_ok(whole)
+
+
+def epilogue(total, xs, ws, bias, dtype):
+    """fl(fl(fl(S) x_scale) w_scale + bias) rounded to `dtype`, all of it exact but the roundings: the product of two
+    binary32 values is exact in binary64, and the sum goes there with its last bit odd if anything is left, so that the
+    rounding to binary32 (29 bits shorter) is that of the exact sum."""
+    p = total.float() * xs[:, None]
+    t, b = p.double() * ws.double(), torch.zeros((), dtype=torch.float64, device="cuda") if bias is None else bias.double()
+    s = t + b
+    back = s - t
+    left = (t - (s - back)) + (b - back)             # what the rounding of t + b dropped
+    bits = s.view(torch.int64)
+    toward = torch.where((left > 0) == (s > 0), 1, -1)
+    odd = torch.where((left != 0) & (bits % 2 == 0), bits + toward, bits)
+    return odd.view(torch.float64).float().to(dtype)
+
+
+BITS = 6506, 10448, (5, 16, 20, 30, 50, 70, 130, 300, 400, 600, 800, 1500)      # N, K, numbers of rows
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_equal_inputs_give_equal_bits(dt, with_bias):
+    """The same rows, alone and among others, through every kind of kernel: the bits of the documented steps."""
+    N, K, counts = BITS
+    kernels = {choice(M, N, K) for M in counts}
+    assert len(kernels) == len(counts)
+    assert {k.rows for k in kernels if k.stream} == {8, 16, 32, 64} and {k.splits for k in kernels} == {1, 2, 4}
+    assert {(k.rows, k.channels) for k in kernels if not k.stream} == {(64, 64), (128, 128), (128, 256), (256, 256)}
+    code, dtype = DT[dt]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    xq, wq, xs, ws = codes(g, max(counts), K), codes(g, N, K), scales(g, max(counts)), scales(g, N)
+    bias = torch.randn(N, device="cuda", generator=g) if with_bias else None
+    total = torch.mm(xq.double(), wq.double().t())   # whole numbers below 2^53: exact
+    want = epilogue(total, xs, ws, bias, dtype)
+    if with_bias:                                    # a product rounded before the sum would show
+        two = ((total.float() * xs[:, None]) * ws + bias).to(dtype)
+        assert bool((two.view(torch.int16) != want.view(torch.int16)).any())
+    for M in counts:
+        nb = lb.lowbit_gemm_w8a8_workspace_bytes(M, N, K)
+        work = torch.empty(max(nb, 1), dtype=torch.uint8, device="cuda")
+        y = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+        lb.check(lb.lowbit_gemm_w8a8(M, N, K, xq, xs, wq, ws, bias, y, code, work, nb))
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want[:M].view(torch.int16)), (M, choice(M, N, K))
+        if not with_bias:                            # by expert: one expert has all rows
+            y.fill_(float("nan"))
+            offs = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+            lb.check(lb.lowbit_moe_gemm_w8a8(1, N, K, wq, ws, xq, xs, M, None, 1, offs, M, y, code))
+            torch.cuda.synchronize()
+            assert torch.equal(y.view(torch.int16), want[:M].view(torch.int16)), (M, choice(M, N, K, 1))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_product_and_bias_have_one_rounding(dt):
+    """A bias that is minus the first row's rounded product leaves what that rounding dropped, and not zero."""
+    N, K, counts = BITS
+    code, dtype = DT[dt]
+    g = torch.Generator(device="cuda").manual_seed(4)
+    xq, wq, xs, ws = codes(g, max(counts), K), codes(g, N, K), scales(g, max(counts)), scales(g, N)
+    total = torch.mm(xq.double(), wq.double().t())
+    bias = -((total[0].float() * xs[0]) * ws)
+    want = epilogue(total, xs, ws, bias, dtype)
+    assert bool((want[0] != 0).float().mean() > 0.5)
+    for M in counts:
+        nb = lb.lowbit_gemm_w8a8_workspace_bytes(M, N, K)
+        work = torch.empty(max(nb, 1), dtype=torch.uint8, device="cuda")
+        y = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+        lb.check(lb.lowbit_gemm_w8a8(M, N, K, xq, xs, wq, ws, bias, y, code, work, nb))
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want[:M].view(torch.int16)), (M, choice(M, N, K))
