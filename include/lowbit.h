@@ -288,9 +288,11 @@ int lowbit_gemv_w4a8_batched_noalloc(int fmt, int M, int group_size, int count, 
  * depend on how the work is split or on M: equal inputs give equal bits.  One
  * entry point for decode and prefill.
  *   M, N, K : any M and N below 2^24 with at most 2^24 - 8 tiles of 256 x 256
- *             outputs (M <= 16: any number); K % 8 == 0 and K <= 131064 (the sum
- *             then fits int32 for codes -128..127), else LOWBIT_E_UNSUPPORTED
+ *             outputs (M <= 16: any number), and K <= 131064 (the sum then fits
+ *             int32 for codes -128..127), else LOWBIT_E_UNSUPPORTED; K % 8 == 0,
+ *             else LOWBIT_E_INVALID_ARG
  *   xq      : i8  [M][K], 16-byte aligned; lowbit_quant_act_i8 makes it and x_scale
+ *             from fp16 rows (so a product whose y it is to quantize writes fp16)
  *   x_scale : f32 [M]
  *   wq      : i8  [N][K], 16-byte aligned, read as it is (no packing)
  *   w_scale : f32 [N]
@@ -560,8 +562,8 @@ int lowbit_moe_layer(const void *w13, const void *w2, int E_local, int E, int H,
  *   workspace      : >= lowbit_moe_sort_workspace_bytes(T, top_k, E_local) bytes,
  *                    256-byte aligned (may be NULL when that is 0); needs no
  *                    clearing, calls that may overlap need one each
- * E and E_local <= 1024, T * top_k < 2^31, else LOWBIT_E_UNSUPPORTED.  Where
- * T * top_k is 0 the offsets are still written.
+ * E and E_local <= 1024, T < 2^24 and T * top_k < 2^31, else
+ * LOWBIT_E_UNSUPPORTED.  Where T * top_k is 0 the offsets are still written.
  */
 int lowbit_moe_sort(const int32_t *topk_ids, int T, int top_k, int E, const int32_t *expert_map, int E_local,
                     int32_t *row_slot, int32_t *slot_row, int32_t *expert_offsets, void *workspace, size_t ws_bytes,
@@ -581,7 +583,8 @@ size_t lowbit_moe_sort_workspace_bytes(int T, int top_k, int E_local);
  *   slot_row          : from lowbit_moe_sort (entries outside [0, T*top_k) count
  *                       as slots without a row)
  * T < 2^24 and T * top_k < 2^31, else LOWBIT_E_UNSUPPORTED (here and below).
- * Its gradient is lowbit_moe_unpermute with weights NULL.
+ * Its gradient for fp16 and bf16 rows is lowbit_moe_unpermute with weights NULL;
+ * there is none for rows of other types.
  */
 int lowbit_moe_permute(const void *x, const float *x_scale, int T, int top_k, int row_bytes, const int32_t *slot_row,
                        void *xp, float *xp_scale, void *stream);
@@ -623,9 +626,14 @@ int lowbit_moe_unpermute_backward(const void *dy, const void *yp, int dtype, con
  *   row_slot   : NULL where the rows of xq lie in expert order (a = r; x_rows >=
  *                rows), or the row_slot of lowbit_moe_sort, i32 [rows], where they
  *                do not: a = row_slot[r] / row_div, row_div being top_k when all
- *                slots of a token read the token's row and 1 when each has its own
+ *                slots of a token read the token's row and 1 when each has its own.
+ *                With x_rows * K of 2^32 and more rows go 16 at a time, their expert's
+ *                weights read again for each 16: slow for many rows
  *   expert_offsets : i32 [E+1], ascending, from lowbit_moe_sort
- *   rows       : rows of y, T*top_k (< 2^24); offsets past it are cut to it
+ *   rows       : rows of y, T*top_k (< 2^24, else LOWBIT_E_UNSUPPORTED); offsets
+ *                past it are cut to it.  The kernel is chosen by rows and E: where
+ *                most slots have no expert here and the caller knows that fewer
+ *                rows exist, passing that smaller number is faster
  *   y          : [rows][N], LOWBIT_F16 or LOWBIT_BF16 (output; must not overlap an input)
  */
 int lowbit_moe_gemm_w8a8(int E, int N, int K, const int8_t *wq, const float *w_scale, const int8_t *xq,
