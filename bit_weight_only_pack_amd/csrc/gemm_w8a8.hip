@@ -275,7 +275,8 @@ __global__ __launch_bounds__(WV * 64) void w8a8_stream_kernel(W8Args p)
 // there are no more); the rows behind them, where an expert has more, are cut
 // into runs of 16 that the remaining rows of the grid share.  They search the
 // runs; the others, whose rows are most or all there are, start at once (128
-// experts of 1536 x 2048, one row each: 45 us, 57 with the search in all).
+// rows that reach some 65 of 128 experts of 1536 x 2048: 39 us; when this was
+// chosen 45, and 57 with the search in all).
 template <int CH, int WV, int NST>
 __global__ __launch_bounds__(WV * 64) void w8a8_stream_experts_kernel(W8Args p)
 {
@@ -880,7 +881,8 @@ void tile_launch(const W8Args &a, int64_t tiles, hipStream_t s)
 // one, a time for K alone.  The constants are fitted to the choice among 3100
 // launches (195 shapes of 371 to 28672 channels, K 192 to 14336 and 69 to 4096
 // rows, unsplit and split; 30 by expert): it takes 0.6 % longer than the best of
-// them on average, 21 % at most.
+// them on average, 21 % at most.  Best of these kernels, that is: the operations
+// or bytes alone would take a third to two thirds of it between 70 and 2200 rows.
 struct W8Cost {
     int rows, channels;
     double ends, step, tile, alone;
@@ -958,7 +960,10 @@ W8Plan w8_plan(int rows, int N, int K)
 }
 
 // A dense product streams the weights where one pass over them serves all rows
-// faster than tiles do: up to 16 rows, and up to 64 by an estimate: a start and
+// faster than tiles do: up to 16 rows (16 rows, stream / tiles, us: 1024 channels
+// of K = 14336 11.0 / 12.4, 4096 of 28672 25.0 / 26.8; tiles are ahead where few
+// channels walk a very long K: 1024 of 28672 19.5 / 15.7, 64 of 131064 107 / 41;
+// one row 12.8 / 14.8 and 62 / 33), and up to 64 by an estimate: a start and
 // an end, then what a workgroup brings to its CU (faster where half of them have
 // none) or the weights from memory.  Measured on 120 shapes of 24 to 64 rows, 200
 // to 8192 channels, K 2048 to 28672, this takes 0.3 % longer than the better of
@@ -1021,21 +1026,31 @@ hipError_t launch_gemm_w8a8(const W8Args &args, void *ws, hipStream_t s)
 }
 
 // Streaming goes by the rows that an expert has on average, tiles by their
-// estimated time; both sides measured (us):
-//   rows an expert                            1        4        8       12       16
-//   128 experts of 1536 x 2048: stream       45       64       66       77       85
-//                               tiles of 64  56       76       79       81       84
-//   8 experts of 4096 x 4096:   stream       16       27       28       30       35
-//                               tiles of 64  17       32       32       32       32
-//   rows an expert                           64                       256
+// estimated time.  Measured (us, weights not in the caches), the same number of
+// rows for every expert:
+//   rows an expert                             1      4      8     12     16
+//   128 experts of 1536 x 2048: stream        65     65     66     72     75     (403 MB: 6.2 TB/s with one row)
+//                               tiles of 64   72     76     77     78     80
+//   8 experts of 4096 x 4096:   stream        27     27     27     28     29
+//                               tiles of 64   32     32     32     32     32
+//   rows an expert                            64                       256
 //   128 experts: tiles of 64 / 128 / 128 x 256 / 256
-//                                           108 / 93 /  90 / 104     257 / 204 / 201 / 216
-//   8 experts                                39 / 35 /  31 /  46      78 /  72 /  67 /  62
-// All 1536 rows of 128 experts with one of them: 50 (tiles of 64: 16).
+//                                             93 / 88 /  88 / 103     243 / 167 / 156 / 148
+//   8 experts                                 34 / 40 /  39 /  53      76 /  53 /  49 /  68
+// The estimate counts half a tile more for every expert: for 256 rows each, all
+// tiles whole, it takes 128 x 256 for the 128 experts and 256 for the 8.  Routed
+// rows, 128 experts of 1536 x 2048, stream / tiles of 64: 128 rows (66 experts
+// reached) 36 / 43, 512 (107) 56 / 64, 1024 (121) 72 / 74, 1536 (122) 92 / 76; all
+// 1536 rows with one of the experts: 46 / 16.
 // A ring of four waves and three stages holds twelve units of K: with fewer of
 // them two waves and two stages serve more workgroups a CU (128 experts of
-// 2048 x 768, 1 / 4 / 8 rows each: 24 / 35 / 36 against 34 / 47 / 50; of
-// 1536 x 2048: 46 / 66 / 69 against 45 / 64 / 66).
+// 2048 x 768, 1 / 4 / 8 rows each: 34 / 35 / 37 against 46 / 47 / 50; of
+// 1536 x 2048: 66 / 68 / 69 against 65 / 65 / 66).
+// Gathered rows of 4 GiB and more stream, however many: 64 / 512 / 4096 rows, 8
+// experts of 4096 x 4096: 24 / 70 / 408 against 25 / 24 / 80 below 4 GiB.
+// `rows` is what y holds, not the rows that exist: with 16 of 128 experts of
+// 1536 x 2048 here and 64 / 256 / 1024 tokens of 8, 13 / 18 / 34 against 10 / 15
+// / 16 with rows cut to those that exist.
 //
 // gathered: rows of x that row_slot picks from, 0 where rows lie in expert order
 static W8Choice experts_choice(int E, int rows, int N, int K, int64_t gathered)
