@@ -882,7 +882,7 @@ void tile_launch(const W8Args &a, int64_t tiles, hipStream_t s)
 // launches (195 shapes of 371 to 28672 channels, K 192 to 14336 and 69 to 4096
 // rows, unsplit and split; 30 by expert): it takes 0.6 % longer than the best of
 // them on average, 21 % at most.  Best of these kernels, that is: the operations
-// or bytes alone would take a third to two thirds of it between 70 and 2200 rows.
+// or bytes alone would take a quarter to two thirds of it between 70 and 2200 rows.
 struct W8Cost {
     int rows, channels;
     double ends, step, tile, alone;
