@@ -33,6 +33,9 @@ def LOWBIT_UINT(bits, asym=False):
 LOWBIT_F16 = 0
 LOWBIT_BF16 = 1
 
+LOWBIT_KV_I8 = 0
+LOWBIT_KV_U4 = 1
+
 LOWBIT_OP_GEMV = 0
 LOWBIT_OP_GEMM = 1
 LOWBIT_OP_GEMV_W4A8 = 2
@@ -55,7 +58,21 @@ class lowbit_gemv_chain(ctypes.Structure):
                 ("spin_limit", ctypes.c_uint), ("buf", ctypes.c_void_p), ("buf_bytes", ctypes.c_size_t)]
 
 
+class lowbit_kv_cache(ctypes.Structure):
+    """Mirror of the C struct of the same name in include/lowbit.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("fmt", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int)]
+
+
+class lowbit_kv_batch(ctypes.Structure):
+    """Mirror of the C struct of the same name in include/lowbit.h."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+                ("table_width", ctypes.c_int), ("count", ctypes.c_int), ("rows", ctypes.c_int),
+                ("max_rows", ctypes.c_int)]
+
+
 _i = ctypes.c_int
+_i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 
 # name -> (restype, argtypes); mirrors include/lowbit.h
@@ -97,6 +114,11 @@ SIGNATURES = {
     "lowbit_moe_permute": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "lowbit_moe_unpermute": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp]),
     "lowbit_moe_unpermute_backward": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "lowbit_kv_page_bytes": (_sz, [_i, _i, _i, _i]),
+    "lowbit_kv_write": (_i, [_vp, _vp, _vp, _i64, _vp, _i64, _i, _vp]),
+    "lowbit_kv_read": (_i, [_vp, _vp, _vp, _i64, _vp, _i64, _i, _vp]),
+    "lowbit_kv_attention": (_i, [_vp, _vp, _vp, _i64, _i, _i, ctypes.c_float, _i, _vp, _vp, _sz, _vp]),
+    "lowbit_kv_attention_workspace_bytes": (_sz, [_vp, _vp, _i]),
     "lowbit_moe_gemm_w8a8": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp]),
 }
 
@@ -348,3 +370,46 @@ def lowbit_moe_gemm_w8a8(E, N, K, wq, w_scale, xq, x_scale, x_rows, row_slot, ro
     return lib().lowbit_moe_gemm_w8a8(E, N, K, _ptr(wq), _ptr(w_scale), _ptr(xq), _ptr(x_scale), x_rows,
                                       _ptr(row_slot), row_div, _ptr(expert_offsets), rows, _ptr(y), y_dtype,
                                       _stream(stream))
+
+
+def lowbit_kv_page_bytes(fmt, page_size, heads, dim):
+    return lib().lowbit_kv_page_bytes(fmt, page_size, heads, dim)
+
+
+def make_kv_cache(data, fmt, pages, page_size, heads, dim):
+    """A lowbit_kv_cache over `data`, which it keeps alive."""
+    c = lowbit_kv_cache(_ptr(data), fmt, pages, page_size, heads, dim)
+    c.keep = data
+    return c
+
+
+def make_kv_batch(page_table, table_width, kv_len, row_offsets, count, rows, max_rows):
+    """A lowbit_kv_batch over device arrays, which it keeps alive."""
+    b = lowbit_kv_batch(_ptr(page_table), _ptr(kv_len), _ptr(row_offsets), table_width, count, rows, max_rows)
+    b.keep = (page_table, kv_len, row_offsets)
+    return b
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def lowbit_kv_write(cache, batch, k, k_stride, v, v_stride, dtype, stream=None):
+    """cache, batch: from make_kv_cache and make_kv_batch (here and below)."""
+    return lib().lowbit_kv_write(_ref(cache), _ref(batch), _ptr(k), k_stride, _ptr(v), v_stride, dtype,
+                                 _stream(stream))
+
+
+def lowbit_kv_read(cache, batch, k, k_stride, v, v_stride, dtype, stream=None):
+    return lib().lowbit_kv_read(_ref(cache), _ref(batch), _ptr(k), k_stride, _ptr(v), v_stride, dtype,
+                                _stream(stream))
+
+
+def lowbit_kv_attention(cache, batch, q, q_stride, q_heads, dtype, scale, window, y, workspace=None, ws_bytes=0,
+                        stream=None):
+    return lib().lowbit_kv_attention(_ref(cache), _ref(batch), _ptr(q), q_stride, q_heads, dtype, scale, window,
+                                     _ptr(y), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def lowbit_kv_attention_workspace_bytes(cache, batch, q_heads):
+    return lib().lowbit_kv_attention_workspace_bytes(_ref(cache), _ref(batch), q_heads)

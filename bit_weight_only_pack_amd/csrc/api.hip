@@ -3,6 +3,9 @@
 // error is detected before the first enqueue.
 #include "lowbit_internal.hpp"
 #include "w8a8_sort.hpp"
+#include "kv_cache.hpp"
+
+#include <cmath>
 
 #include <vector>
 
@@ -852,6 +855,121 @@ int lowbit_moe_gemm_w8a8(int E, int N, int K, const int8_t *wq, const float *w_s
     const W8Args a = {xq, wq, x_scale, w_scale, nullptr, y, row_slot, expert_offsets, rows, N, K, E, x_rows,
                       row_slot != nullptr ? row_div : 1, y_dtype == LOWBIT_BF16};
     return hip_status(launch_moe_gemm_w8a8(a, (hipStream_t)stream));
+}
+
+namespace {
+bool kv_shape_ok(int fmt, int page_size, int heads, int dim)
+{
+    return (fmt == LOWBIT_KV_I8 || fmt == LOWBIT_KV_U4) && (page_size == 64 || page_size == 128 || page_size == 256) &&
+           (dim == 64 || dim == 128 || dim == 256) && heads > 0 && heads <= kKvMaxHeads;
+}
+
+// Checks shared by the entry points of the key/value cache.  *empty: there is nothing to do.
+int check_kv(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool *empty)
+{
+    *empty = false;
+    if (c == nullptr || b == nullptr) return LOWBIT_E_INVALID_ARG;
+    if (c->pages < 0 || c->heads <= 0 || b->table_width < 0 || b->count < 0 || b->rows < 0 || b->max_rows < 0)
+        return LOWBIT_E_INVALID_ARG;
+    if (!kv_shape_ok(c->fmt, c->page_size, c->heads, c->dim)) return LOWBIT_E_UNSUPPORTED;
+    if ((int64_t)b->table_width * c->page_size > ((int64_t)1 << 30) || b->count >= kGridLimit)
+        return LOWBIT_E_UNSUPPORTED;
+    if (b->count == 0 || b->rows == 0 || b->max_rows == 0) {
+        *empty = true;
+        return LOWBIT_OK;
+    }
+    if (b->kv_len == nullptr || b->row_offsets == nullptr || (b->table_width > 0 && b->page_table == nullptr) ||
+        (c->pages > 0 && c->data == nullptr))
+        return LOWBIT_E_INVALID_ARG;
+    if (!aligned(c->data, 256) || !aligned(b->page_table, 4) || !aligned(b->kv_len, 4) || !aligned(b->row_offsets, 4))
+        return LOWBIT_E_INVALID_ARG;
+    a->data = static_cast<uint8_t *>(c->data);
+    a->table = b->page_table;
+    a->len = b->kv_len;
+    a->offsets = b->row_offsets;
+    a->fmt = c->fmt;
+    a->pages = c->pages;
+    a->page_shift = c->page_size == 64 ? 6 : c->page_size == 128 ? 7 : 8;
+    a->heads = c->heads;
+    a->dim = c->dim;
+    a->part = kv_part_bytes(c->fmt, c->page_size, c->dim);
+    a->width = b->table_width;
+    a->count = b->count;
+    a->rows = b->rows;
+    a->max_rows = b->max_rows < b->rows ? b->max_rows : b->rows;
+    return LOWBIT_OK;
+}
+
+int check_kv_rows(const KvArgs &a, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype)
+{
+    if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16) return LOWBIT_E_UNSUPPORTED;
+    const int64_t row = (int64_t)a.heads * a.dim;
+    if (k == nullptr || v == nullptr || k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+        !aligned(k, 16) || !aligned(v, 16))
+        return LOWBIT_E_INVALID_ARG;
+    return kv_rows_fit(a) ? LOWBIT_OK : LOWBIT_E_UNSUPPORTED;
+}
+}  // namespace
+
+size_t lowbit_kv_page_bytes(int fmt, int page_size, int heads, int dim)
+{
+    return kv_shape_ok(fmt, page_size, heads, dim) ? (size_t)heads * kv_part_bytes(fmt, page_size, dim) : 0;
+}
+
+int lowbit_kv_write(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, const void *k, int64_t k_stride,
+                    const void *v, int64_t v_stride, int dtype, void *stream)
+{
+    KvArgs a{};
+    bool empty;
+    int st = check_kv(cache, batch, &a, &empty);
+    if (st != LOWBIT_OK || empty) return st;
+    st = check_kv_rows(a, k, k_stride, v, v_stride, dtype);
+    if (st != LOWBIT_OK) return st;
+    return hip_status(launch_kv_write(a, k, k_stride, v, v_stride, dtype == LOWBIT_BF16, (hipStream_t)stream));
+}
+
+int lowbit_kv_read(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, void *k, int64_t k_stride, void *v,
+                   int64_t v_stride, int dtype, void *stream)
+{
+    KvArgs a{};
+    bool empty;
+    int st = check_kv(cache, batch, &a, &empty);
+    if (st != LOWBIT_OK || empty) return st;
+    st = check_kv_rows(a, k, k_stride, v, v_stride, dtype);
+    if (st != LOWBIT_OK) return st;
+    return hip_status(launch_kv_read(a, k, k_stride, v, v_stride, dtype == LOWBIT_BF16, (hipStream_t)stream));
+}
+
+size_t lowbit_kv_attention_workspace_bytes(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, int q_heads)
+{
+    KvArgs a{};
+    bool empty;
+    if (check_kv(cache, batch, &a, &empty) != LOWBIT_OK || empty) return 0;
+    if (q_heads <= 0 || q_heads % a.heads != 0 || q_heads > kKvMaxHeads || !kv_attention_fits(a, q_heads)) return 0;
+    return kv_attention_workspace(a, q_heads);
+}
+
+int lowbit_kv_attention(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, const void *q, int64_t q_stride,
+                        int q_heads, int dtype, float scale, int window, void *y, void *workspace, size_t ws_bytes,
+                        void *stream)
+{
+    KvArgs a{};
+    bool empty;
+    const int st = check_kv(cache, batch, &a, &empty);
+    if (st != LOWBIT_OK) return st;
+    if (q_heads <= 0 || q_heads % cache->heads != 0 || window < 0 || !std::isfinite(scale) || !(scale > 0.f))
+        return LOWBIT_E_INVALID_ARG;
+    if (q_heads > kKvMaxHeads || (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16)) return LOWBIT_E_UNSUPPORTED;
+    if (empty) return LOWBIT_OK;
+    if (q == nullptr || y == nullptr || q_stride < (int64_t)q_heads * a.dim || q_stride % 8 != 0 || !aligned(q, 16) ||
+        !aligned(y, 16))
+        return LOWBIT_E_INVALID_ARG;
+    if (!kv_attention_fits(a, q_heads)) return LOWBIT_E_UNSUPPORTED;
+    const size_t need = kv_attention_workspace(a, q_heads);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LOWBIT_E_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return LOWBIT_E_INVALID_ARG;
+    return hip_status(launch_kv_attention(a, q, q_stride, q_heads, dtype == LOWBIT_BF16, scale, window, y, workspace,
+                                          (hipStream_t)stream));
 }
 
 }  // extern "C"

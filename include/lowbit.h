@@ -640,6 +640,131 @@ int lowbit_moe_gemm_w8a8(int E, int N, int K, const int8_t *wq, const float *w_s
                          const float *x_scale, int x_rows, const int32_t *row_slot, int row_div,
                          const int32_t *expert_offsets, int rows, void *y, int y_dtype, void *stream);
 
+/* ---- key/value cache formats -------------------------------------------- */
+#define LOWBIT_KV_I8  0  /* 8-bit codes, fp32 scale per token and head             */
+#define LOWBIT_KV_U4  1  /* 4-bit codes, fp32 scale and minimum per token and head */
+
+/*
+ * A key/value cache in pages of a few tokens, held in 8 or 4 bits: the other
+ * low-bit operand of a decoder step.  lowbit_kv_write quantises new tokens into
+ * it, lowbit_kv_read brings them back, lowbit_kv_attention multiplies with it,
+ * unpacking in registers as the products with low-bit weights do ("Low Bit ARM
+ * kernels": 8- and 4-bit codes with a scale per group, unpacked just before
+ * use; the cache, its formats and its layout are this library's).
+ *
+ * Quantised row: the dim values x of one token and one head, in binary32.
+ *   LOWBIT_KV_I8: amax = max |x|, scale = fl(amax / 127),
+ *     code = rne(fl(x * min(fl(127 / amax), FLT_MAX))) in [-127, 127];  value = code * scale
+ *   LOWBIT_KV_U4: lo = min x, h = fl(max x / 2 - lo / 2), scale = fl(h / 7.5),
+ *     code = rne(fl(fl(x / 2 - lo / 2) * min(fl(15 / h), FLT_MAX))) in [0, 15];
+ *     value = code * scale + lo
+ *   A row of equal values (I8: of zeros) gets scale 0 and codes 0.  A row with
+ *   an infinity or a NaN gets scale NaN (codes 0, minimum 0): it reads back as
+ *   NaN, and attention that sees its token returns NaN.
+ *
+ * Page: page_size tokens of all heads; lowbit_kv_page_bytes / heads bytes for
+ * each head, in this order: K codes, V codes, then arrays f32 [page_size]: K
+ * scale, V scale (I8) or K scale, K minimum, V scale, V minimum (U4).  Codes lie
+ * in the order in which the matrix cores take them:
+ *   I8, a byte holds code + 128:
+ *     K of token t, dim d: ((t/16 * dim/64 + d/64) * 4 + d%64/16) * 256 + t%16 * 16 + d%16
+ *     V of token t, dim d: ((t/64 * dim/16 + d/16) * 4 + t%16/4) * 256 + d%16 * 16 + t%64/16 * 4 + t%4
+ *   U4, a byte holds two codes of one token:
+ *     K: byte ((t/32 * dim/64 + d/64) * 4 + d%64/16) * 256 + t%16 * 16 + t%32/16 * 8 + d%16/8 * 4 + i, where
+ *        i = 0, 1, 2, 3 for the dims d%8 = (0, 2), (4, 6), (1, 3), (5, 7), the lower nibble first
+ *     V: byte ((t/64 * dim/32 + d/32) * 4 + t%16/4) * 256 + d%16 * 16 + t%64/16 * 4 + t%4, lower nibble d%32 < 16
+ */
+typedef struct lowbit_kv_cache {
+    void *data;      /* device [pages][lowbit_kv_page_bytes(...)], 256-byte aligned */
+    int fmt;         /* LOWBIT_KV_I8 or LOWBIT_KV_U4                                */
+    int pages;       /* pages that data holds                                       */
+    int page_size;   /* tokens of a page: 64, 128 or 256                            */
+    int heads;       /* key/value heads                                             */
+    int dim;         /* values of a head: 64, 128 or 256                            */
+} lowbit_kv_cache;
+
+/*
+ * The sequences of a call.  Sequence b has kv_len[b] tokens, the new ones
+ * included; token p lies in page page_table[b][p / page_size] at place p %
+ * page_size.  Its rows of the call's matrices are row_offsets[b] .. row_offsets[b
+ * + 1] - 1, and they stand for its last tokens: the last row is token kv_len[b] -
+ * 1.  All three arrays are read by the kernels (a captured graph takes new
+ * lengths and pages at each replay), so they are checked there:
+ *   - a page_table entry outside [0, pages) and a token past table_width *
+ *     page_size have no page: not written, read as zeros, not seen by attention;
+ *   - a row that would stand before token 0 is not written, is read as zeros, and
+ *     its attention is zeros, as is that of any row that sees no token;
+ *   - offsets are cut to [0, rows]; rows of no sequence are left as they were.
+ * A page may be shared by sequences that read it.  Where two rows of one
+ * lowbit_kv_write stand for the same place of the same page, what the place
+ * holds afterwards is undefined.
+ */
+typedef struct lowbit_kv_batch {
+    const int32_t *page_table;   /* device i32 [count][table_width]                              */
+    const int32_t *kv_len;       /* device i32 [count]                                           */
+    const int32_t *row_offsets;  /* device i32 [count + 1], ascending                            */
+    int table_width;             /* table_width * page_size <= 2^30, else LOWBIT_E_UNSUPPORTED   */
+    int count;                   /* sequences                                                    */
+    int rows;                    /* rows of the call's matrices                                  */
+    int max_rows;                /* at least the most rows that one sequence has: sizes the grid
+                                    (rows of a sequence past it are left out)                    */
+} lowbit_kv_batch;
+
+/* Bytes of one page (0 for an invalid combination; a multiple of 256 * heads). */
+size_t lowbit_kv_page_bytes(int fmt, int page_size, int heads, int dim);
+
+/*
+ * Quantise the rows of k and v into their places of the cache.  `cache` and
+ * `batch` (and below) are HOST structs, read during the call.
+ *   k, v   : [rows] rows of heads * dim values, LOWBIT_F16 or LOWBIT_BF16, 16-byte
+ *            aligned, k_stride and v_stride values apart (at least heads * dim, a
+ *            multiple of 8): slices of a stacked projection's output go in as they are
+ * Other tokens of the pages keep what they held.
+ */
+int lowbit_kv_write(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, const void *k, int64_t k_stride,
+                    const void *v, int64_t v_stride, int dtype, void *stream);
+
+/*
+ * The reverse: the values that the cache holds of the tokens that the rows stand
+ * for, each rounded to nearest even into dtype (of the fp32 product, or fused
+ * product and sum, of code, scale and minimum).  With row_offsets that give every
+ * sequence kv_len[b] rows it reads them whole.
+ *   k, v : as above (outputs)
+ */
+int lowbit_kv_read(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, void *k, int64_t k_stride, void *v,
+                   int64_t v_stride, int dtype, void *stream);
+
+/*
+ * Attention of the rows' queries over their sequences' cached tokens:
+ *   y[r][h] = RNE( sum_j p_j v[j][h / group] ),  p = softmax_j( scale * sum_d q[r][h][d] * k[j][h / group][d] )
+ * over the tokens j <= t and, with window > 0, j > t - window, t being the token
+ * that row r stands for; group = q_heads / heads; k and v are the values that the
+ * cache holds.  One entry point for single tokens, drafted tokens and prompts;
+ * the rows of the call have been written before (lowbit_kv_write).
+ * Sums, maxima and the softmax are held in fp32; p is rounded to fp16 for the
+ * matrix cores (q too if it is bf16, after a power of two of its row: values
+ * below 2^-28 of the row's largest lose bits).
+ *   q         : [rows] rows of q_heads * dim values, LOWBIT_F16 or LOWBIT_BF16,
+ *               16-byte aligned, q_stride values apart (at least q_heads * dim, a
+ *               multiple of 8)
+ *   q_heads   : a multiple of heads; head h reads the cache's head h / (q_heads / heads)
+ *   scale     : finite and > 0
+ *   window    : tokens that a row sees at most, its own included; 0: no limit
+ *   y         : [rows][q_heads * dim] of the same type (output), 16-byte aligned;
+ *               must not overlap q
+ *   workspace : >= lowbit_kv_attention_workspace_bytes(cache, batch, q_heads) bytes,
+ *               256-byte aligned (partial results where few rows share out the
+ *               tokens; may be NULL when that is 0).  Nothing in it outlives the
+ *               call, and it needs no clearing; calls that may overlap need one each.
+ */
+int lowbit_kv_attention(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, const void *q, int64_t q_stride,
+                        int q_heads, int dtype, float scale, int window, void *y, void *workspace, size_t ws_bytes,
+                        void *stream);
+
+/* Workspace bytes of lowbit_kv_attention (0 if none is needed or the sizes are
+ * invalid).  It depends on the sizes alone: not on lengths, pages or offsets. */
+size_t lowbit_kv_attention_workspace_bytes(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, int q_heads);
+
 #ifdef __cplusplus
 }
 #endif
