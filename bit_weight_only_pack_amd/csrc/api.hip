@@ -893,7 +893,7 @@ int check_kv(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool
     a->heads = c->heads;
     a->dim = c->dim;
     a->part = kv_part_bytes(c->fmt, c->page_size, c->dim);
-    a->width = b->table_width;
+    a->width = c->pages > 0 ? b->table_width : 0;     // without pages no token has one
     a->count = b->count;
     a->rows = b->rows;
     a->max_rows = b->max_rows < b->rows ? b->max_rows : b->rows;
