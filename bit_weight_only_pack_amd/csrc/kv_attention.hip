@@ -28,8 +28,11 @@ namespace lowbit {
 
 namespace {
 
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTile = 64;                // tokens of a step: one block of a page
+constexpr int kMaxItems = 512;           // items that are cut into pieces
 constexpr int kMinPiece = 4;             // blocks that a workgroup takes at least: one for each wave
 
 struct AttnArgs {
@@ -42,9 +45,9 @@ struct AttnArgs {
     int tiles;                           // row tiles of a sequence; item = sequence * tiles + tile
     int64_t over, upto;                  // sequences of over < n * group <= upto rows are this launch's
     int share;                           // 0: a workgroup takes an item's tokens whole; else pieces that they make, items aside
-    float *part_o;                       // [pieces][heads][rows][dim]
-    float2 *part_ml;                     // [pieces][heads][rows]: maximum and sum of each row's softmax
-    int2 *parts;                         // [items]: first piece and how many, left by the first piece's workgroup
+    float *part_o;                       // [slots][heads][rows][dim]
+    float2 *part_ml;                     // [slots][heads][rows]: maximum and sum of each row's softmax
+    int4 *cuts;                          // [0]: how many items are cut; then item, first slot and pieces of each
 };
 
 // What a row tile of a sequence works on
@@ -81,62 +84,78 @@ __device__ __forceinline__ Span attn_span(const AttnArgs &a, int b, int tile, in
     return attn_rows(a, s, tile * rows, ours ? (int)min((int64_t)rows, all - tile * rows) : 0);
 }
 
-// The items' tokens cut into pieces of equal size, so that workgroups end
-// together whatever the lengths are: with `share` pieces' worth of blocks in all,
-// an item of n blocks makes ceil(n / size) pieces, at most share + items of them.
-// Every wave works this out for itself from the lengths, 64 items at a time.
+// The items' tokens cut into pieces of equal size, so that workgroups end together whatever the lengths are: with `share`
+// pieces' worth of blocks in all, an item of n blocks makes ceil(n / size) pieces, at most share + items of them; those of
+// items that are cut, at most 2 * share, have slots for their results.  Nothing is cut where no item is much longer than a
+// piece.  Every wave works this out for itself from the lengths, 64 items at a time.
 struct Piece {
-    int item, piece, first;              // the item, which of its pieces, number of its first piece
+    int item, piece;                     // the item, which of its pieces
     int count, size;                     // its pieces, blocks of a piece
+    int slot;                            // slot of its first piece
+    int cut, cuts;                       // which of the items that are cut, how many there are
 };
-__device__ __forceinline__ int item_blocks(const AttnArgs &a, int item, int rows, bool &any)
+__device__ __forceinline__ int item_blocks(const AttnArgs &a, int item, int rows)
 {
-    any = false;
-    if (item >= a.kv.count * a.tiles) return 0;
+    if (item >= a.kv.count * a.tiles) return -1;
     const Span t = attn_span(a, item / a.tiles, item % a.tiles, rows);
-    any = t.nr > 0;
-    return any ? t.end - t.first : 0;
+    return t.nr > 0 ? t.end - t.first : -1;
 }
-__device__ __forceinline__ int wave_sum(int v)
+// the sum of the lanes below and of the lane's own
+__device__ __forceinline__ int wave_scan(int v)
 {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        v += lane >= d ? u : 0;
+    }
     return v;
 }
 // the piece of number `want`; false: there is none
 __device__ __forceinline__ bool find_piece(const AttnArgs &a, int rows, int want, Piece &o)
 {
+    constexpr int CHUNKS = kMaxItems / 64;
     const int lane = threadIdx.x & 63, items = a.kv.count * a.tiles;
-    bool any;
-    int n = item_blocks(a, lane, rows, any);
-    int64_t total = wave_sum(n);
-    for (int base = 64; base < items; base += 64) {
-        bool more;
-        total += wave_sum(item_blocks(a, base + lane, rows, more));
-    }
-    o.size = (int)max((total + a.share - 1) / a.share, (int64_t)kMinPiece);
-    int before = 0;
-    for (int base = 0; base < items; base += 64) {
-        if (base > 0) n = item_blocks(a, base + lane, rows, any);
-        const int mine = any ? max((n + o.size - 1) / o.size, 1) : 0;
-        int upto = mine;
+    int n[CHUNKS], most = 0;
+    uint32_t total = 0;                              // in fours: an item has up to 2^24 blocks
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(upto, d);
-            if (lane >= d) upto += v;
-        }
+    for (int c = 0; c < CHUNKS; ++c) {
+        n[c] = c * 64 < items ? item_blocks(a, c * 64 + lane, rows) : -1;
+        total += (uint32_t)(max(n[c], 0) + 3) >> 2;
+        most = max(most, n[c]);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        total += __shfl_xor(total, d);
+        most = max(most, __shfl_xor(most, d));
+    }
+    const int even = max((int)((((int64_t)total << 2) + a.share - 1) / a.share), kMinPiece);
+    o.size = __builtin_amdgcn_readfirstlane(most <= even + even / 2 ? max(most, 1) : even);
+    int before = 0, slots = 0;
+    o.cuts = 0;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) o.cuts += __popcll(__ballot(n[c] > o.size));
+    o.cut = 0;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        if (c * 64 >= items) break;
+        const uint64_t cut = __ballot(n[c] > o.size);
+        const int mine = n[c] < 0 ? 0 : max((n[c] + o.size - 1) / o.size, 1), kept = mine > 1 ? mine : 0;
+        const int upto = wave_scan(mine), kept_upto = wave_scan(kept);
         const int first = before + upto - mine;
         const uint64_t hit = __ballot((first <= want) & (want < first + mine));
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
-            o.item = base + l;
-            o.first = __builtin_amdgcn_readlane(first, l);
+            o.item = c * 64 + l;
+            o.piece = want - __builtin_amdgcn_readlane(first, l);
             o.count = __builtin_amdgcn_readlane(mine, l);
-            o.piece = want - o.first;
-            o.size = __builtin_amdgcn_readfirstlane(o.size);
+            o.slot = __builtin_amdgcn_readlane(slots + kept_upto - kept, l);
+            o.cut += __popcll(cut & (((uint64_t)1 << l) - 1));
             return true;
         }
+        o.cut += __popcll(cut);
         before += __builtin_amdgcn_readlane(upto, 63);
+        slots += __builtin_amdgcn_readlane(kept_upto, 63);
     }
     return false;
 }
@@ -152,7 +171,7 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 
 // 4 dims of a finished row: into y where its item is one piece, else among the pieces' results
 template <int D, bool BF16>
-__device__ __forceinline__ void put_result(const AttnArgs &a, const Span &t, int pieces, int number, int kvh, int rows,
+__device__ __forceinline__ void put_result(const AttnArgs &a, const Span &t, int pieces, int slot, int kvh, int rows,
                                            int rr, int d, f4 v, float top, float sum)
 {
     if (pieces == 1) {
@@ -160,7 +179,7 @@ __device__ __forceinline__ void put_result(const AttnArgs &a, const Span &t, int
         const ushort4 w = {round_out<BF16>(v[0]), round_out<BF16>(v[1]), round_out<BF16>(v[2]), round_out<BF16>(v[3])};
         *reinterpret_cast<ushort4 *>(a.y + ((int64_t)(t.s.row0 + i) * a.q_heads + kvh * a.group + h) * D + d) = w;
     } else {
-        const int64_t p = ((int64_t)number * a.kv.heads + kvh) * rows + rr;
+        const int64_t p = ((int64_t)slot * a.kv.heads + kvh) * rows + rr;
         *reinterpret_cast<f4 *>(a.part_o + p * D + d) = v;
         if (d == 0) a.part_ml[p] = float2{top, sum};
     }
@@ -235,6 +254,9 @@ struct Codes {
 
 __device__ __forceinline__ bool inside(int at, int lo, int hi) { return (at >= lo) & (at < hi); }
 
+// the larger of `top` and |v|, if v is finite
+__device__ __forceinline__ float finite_max(float top, float v) { return fabsf(v) <= FLT_MAX ? fmaxf(top, fabsf(v)) : top; }
+
 // largest over the four lanes of a column (l, l ^ 16, l ^ 32, l ^ 48): swaps of lane rows, no LDS
 __device__ __forceinline__ float column_max(float v)
 {
@@ -242,6 +264,11 @@ __device__ __forceinline__ float column_max(float v)
     v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
     p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v)
+{
+    return fmaxf(v, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xf, 0xf, true)));
 }
 __device__ __forceinline__ float column_sum(float v)
 {
@@ -292,192 +319,284 @@ struct BlockRegs {
 constexpr float kSlack = 8.f;
 constexpr int kTop = 6;
 
-// 16 * NQ rows of an item as a wave holds them, and what they have summed up so far.  A lane's column is row 16 x + l % 16.
-template <int FMT, int D, bool BF16, int NQ>
+// How a matrix instruction lays things out: COLS = 16 (16x16x32) or 32 (32x32x16) rows of the item are its columns; a lane
+// l has column l % COLS and, j being l / COLS, the tokens (64 / QN) * q + 4 j + e of a block, q < QN and e < 4, and as many
+// dims of each result.
+template <int COLS>
+struct Shape;
+template <>
+struct Shape<16> {
+    typedef f4 Acc;
+    static constexpr int QN = 4, STEP = 32, TILES = 4, EL = 4;      // STEP: dims (tokens) that an instruction sums over
+    static __device__ __forceinline__ f4 mul(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ float max_of(float v) { return column_max(v); }
+    static __device__ __forceinline__ float sum_of(float v) { return column_sum(v); }
+};
+template <>
+struct Shape<32> {
+    typedef float Acc __attribute__((ext_vector_type(16)));
+    static constexpr int QN = 8, STEP = 16, TILES = 2, EL = 16;
+    static __device__ __forceinline__ Acc mul(h8 a, h8 b, Acc c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ float max_of(float v)
+    {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    }
+    static __device__ __forceinline__ float sum_of(float v) { return v + __shfl_xor(v, 32); }
+};
+
+// COLS * NQ rows of an item as a wave holds them, and what they have summed up so far.
+// EVEN: the keys' scales come multiplied by what makes a product of codes and operands an exponent of base 2, for all rows
+// alike unless the rows differ too much; else every row has its own factor.
+template <int FMT, int D, bool BF16, int COLS, int NQ, bool EVEN>
 struct Rows {
+    typedef Shape<COLS> S;
+    typedef typename S::Acc Acc;
     static constexpr bool I8 = FMT == LOWBIT_KV_I8;
-    static constexpr int KS = D / 32, M = D / 16;
+    static constexpr int KS = D / S::STEP, M = D / COLS, EL = S::EL, QN = S::QN, PU = 64 / S::STEP;
     typedef Codes<FMT, D> C;
     h8 qf[NQ][KS];
-    float c[NQ], qsum[NQ];               // scale * log2(e) / (what the row's queries were multiplied by); their sum
+    float c[NQ], qsum[NQ];               // the row's factor of the scales; the sum of its operands
+    bool alike;                          // EVEN: all factors are 1
     int see_lo[NQ], see_hi[NQ];          // tokens that the row sees
-    f4 o[NQ][M];                         // sum p * vscale * 2^(kTop - E) * code, 4 dims of the lane's column
-    float m[NQ], mc[NQ], l[NQ], bias[NQ];// maximum of s, that times c, sums of the lane's p and p * vmin
+    Acc o[NQ][M];                        // sum p * vscale * 2^(kTop - E) * code, EL dims of the lane's column
+    float mc[NQ], limit[NQ];             // exponent that the row's terms are taken to, and what they may pass it by
+    float l[NQ], bias[NQ];               // sums of the lane's p and p * vmin
     int E;
 
-    // rows r0 .. of the item, nr of them there
-    __device__ __forceinline__ void load(const AttnArgs &a, const KvSeq &seq, int kvh, int r0, int nr, int lane)
+    // first of the 8 dims that lanes j have in step k
+    static __device__ __forceinline__ int dims(int k, int j)
     {
-        const int j = lane >> 4, n = lane & 15;
+        return COLS == 16 ? k / 2 * 64 + 16 * j + k % 2 * 8 : 16 * k + 8 * j;
+    }
+    __device__ __forceinline__ void scale_sums(int x, float f)
+    {
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) o[x][i][e] *= f;
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int e = 0; e < EL; ++e) o[x][i][e] = 0.f;
+    }
+
+    // Rows r0 .. of the item, nr of them there.  Returns what the scales of all rows are to be multiplied by (EVEN); the
+    // rows of bf16 of all waves then need `meet`, which gives a value's largest and smallest over the workgroup.
+    template <typename F>
+    __device__ __forceinline__ float load(const AttnArgs &a, const KvSeq &seq, int kvh, int r0, int nr, int lane, F meet)
+    {
+        const int j = lane / COLS, n = lane % COLS;
+        us8 raw[NQ][KS];
+        int top[NQ];                     // largest |q| of the row, its bits; 0 where there is none or no number
+        float all = a.scale2;
+        alike = true;
+        E = -100;
+        clear();
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
-            const int r = r0 + (x * 16 + n < nr ? x * 16 + n : 0), i = r / a.group, h = r % a.group;
-            const uint16_t *src = a.q + (int64_t)(seq.row0 + i) * a.q_stride + (kvh * a.group + h) * D + 16 * j;
+            const int r = r0 + (x * COLS + n < nr ? x * COLS + n : 0), i = r / a.group, h = r % a.group;
+            const uint16_t *src = a.q + (int64_t)(seq.row0 + i) * a.q_stride + (kvh * a.group + h) * D;
             see_hi[x] = seq.pos0 + i + 1;
             see_lo[x] = a.window > 0 ? see_hi[x] - min(a.window, max(seq.len, 1)) : 0;
-            us8 raw[KS];
 #pragma unroll
-            for (int k = 0; k < KS; ++k) raw[k] = *reinterpret_cast<const us8 *>(src + k / 2 * 64 + k % 2 * 8);
-            c[x] = a.scale2;
+            for (int k = 0; k < KS; ++k) raw[x][k] = *reinterpret_cast<const us8 *>(src + dims(k, j));
+            c[x] = EVEN ? 1.f : a.scale2;
+            qsum[x] = l[x] = bias[x] = mc[x] = 0.f;
+            limit[x] = -INFINITY;
             if constexpr (BF16) {
-                // into fp16 after a power of two that brings the row's largest value to [2^14, 2^15)
-                uint32_t top = 0;
+                top[x] = 0;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, (uint32_t)raw[k][e] & 0x7fffu);
-                top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-                top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-                const int shift = top == 0 || top >= 0x7f80u ? 0 : 141 - (int)(top >> 7);
+                    for (int e = 0; e < 8; ++e) top[x] = max(top[x], raw[x][k][e] & 0x7fff);
+                if (COLS == 16) top[x] = max(top[x], __shfl_xor(top[x], 16));
+                top[x] = max(top[x], __shfl_xor(top[x], 32));
+                if (top[x] >= 0x7f80) top[x] = 0;
+            }
+        }
+        if constexpr (BF16) {
+            // into fp16 after a power of two that brings the largest value of the row, or of all rows if none's is smaller
+            // by more than 2^8, to [2^14, 2^15)
+            int shift_all = 0;
+            if constexpr (EVEN) {
+                int hi = 0, lo = 0x7fff;
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    hi = max(hi, top[x]);
+                    lo = top[x] > 0 ? min(lo, top[x]) : lo;
+                }
+                meet(hi, lo);
+                alike = lo >= hi || (hi >> 7) - (lo >> 7) <= 8;
+                shift_all = hi > 0 ? 141 - (hi >> 7) : 0;
+                if (alike) all = ldexpf(all, -shift_all);
+            }
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                const int own = top[x] > 0 ? 141 - (top[x] >> 7) : 0, shift = EVEN && alike ? shift_all : own;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        qf[x][k][e] = (_Float16)ldexpf(__uint_as_float((uint32_t)raw[k][e] << 16), shift);
-                c[x] = ldexpf(c[x], -shift);
-            } else {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) qf[x][k] = __builtin_bit_cast(h8, raw[k]);
+                        qf[x][k][e] = (_Float16)ldexpf(__uint_as_float((uint32_t)raw[x][k][e] << 16), shift);
+                if (!EVEN || !alike) c[x] = ldexpf(c[x], -own);
             }
-            c[x] = fminf(fmaxf(c[x], FLT_MIN), FLT_MAX);
-            qsum[x] = 0.f;
+        } else {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) qf[x][k] = __builtin_bit_cast(h8, raw[x][k]);
+        }
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            if constexpr (!EVEN) c[x] = fminf(fmaxf(c[x], FLT_MIN), FLT_MAX);
             if constexpr (!I8) {
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) qsum[x] += (float)qf[x][k][e];
-                qsum[x] = column_sum(qsum[x]);
+                qsum[x] = S::sum_of(qsum[x]);
             }
-#pragma unroll
-            for (int i = 0; i < M; ++i) o[x][i] = f4{0.f, 0.f, 0.f, 0.f};
-            m[x] = -INFINITY;
-            mc[x] = l[x] = bias[x] = 0.f;
         }
-        E = -100;
+        return fminf(fmaxf(all, FLT_MIN), FLT_MAX);
     }
 
-    // s: products of the queries with a block's codes (tokens 16 q + 4 j + e); leaves the operand of the product with its
-    // values.  kl, vl (4 bits): minima + 8 scales.  masked: some row does not see all of the block, whose first token is
-    // t0; it has tokens that some row sees in [some_lo, some_hi).
-    __device__ __forceinline__ void weigh(f4 (&s)[NQ][4], const f4 (&ks)[4], const f4 *kl, f4 (&vs)[4], f4 *vl,
-                                          bool masked, bool paged, int64_t t0, int some_lo, int some_hi, int j,
-                                          h8 (&pf)[NQ][2])
+    // takes the sums to another exponent of the value scales
+    __device__ __forceinline__ void move_to(int e)
     {
-        if (masked) {
-            // tokens that no row sees: their scales do not count
+        if (e == E) return;
+        const float f = ldexpf(1.f, E - e);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+        for (int x = 0; x < NQ; ++x) scale_sums(x, f);
+        E = e;
+    }
+
+    // acc: products of the queries with a block's codes; leaves the operand of the product with its values.  kl, vl (4
+    // bits): minima + 8 scales (the keys' with the factor of their scales); vs: times 2^(kTop - E).
+    // masked: some row does not see all of the block, whose first token is t0, or its page is missing.
+    template <typename KS_, typename KL, typename VS, typename VL>
+    __device__ __forceinline__ void weigh(Acc (&acc)[NQ][S::TILES], KS_ ks, KL kl, VS vs, VL vl, bool masked, bool paged,
+                                          int64_t t0, int j, h8 (&pf)[NQ][PU])
+    {
+        constexpr int T = 64 / QN;       // tokens from one q to the next
+        auto s = [&](int x, int q, int e) -> float { return acc[x][q * 4 / EL][q * 4 % EL + e]; };
+        auto put = [&](int x, int q, int e, float v) { acc[x][q * 4 / EL][q * 4 % EL + e] = v; };
+        // exponents, less the one that the row's terms are taken to
+        if (EVEN && alike) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int at = 16 * q + 4 * j + e;
-                    vs[q][e] = inside(at, some_lo, some_hi) ? vs[q][e] : 0.f;
-                }
+            for (int q = 0; q < QN; ++q) {
+                const f4 kq = ks(q), lq = I8 ? f4{} : kl(q);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        put(x, q, e, __builtin_fmaf(s(x, q, e), kq[e],
+                                                    I8 ? -mc[x] : __builtin_fmaf(lq[e], qsum[x], -mc[x])));
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                const f4 kq = ks(q), lq = I8 ? f4{} : kl(q);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        put(x, q, e, __builtin_fmaf(s(x, q, e), kq[e] * c[x],
+                                                    I8 ? -mc[x] : __builtin_fmaf(lq[e] * c[x], qsum[x], -mc[x])));
+            }
         }
-        // value scales: the largest exponent so far, infinities and NaN aside
-        float v_top = 0.f;
+        // tokens of the block that the lane's rows see, from its own first
+        int lo[NQ], hi[NQ];
+        if (masked)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+            for (int x = 0; x < NQ; ++x) {
+                lo[x] = (int)min(max((int64_t)see_lo[x] - t0, (int64_t)0), (int64_t)kTile) - 4 * j;
+                hi[x] = (paged ? (int)min(max((int64_t)see_hi[x] - t0, (int64_t)0), (int64_t)kTile) : 0) - 4 * j;
 #pragma unroll
-            for (int e = 0; e < 4; e += 2)       // as fmaxf would, without quieting what was loaded first
-                asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(v_top) : "v"(vs[q][e]), "v"(vs[q][e + 1]));
-        v_top = column_max(v_top);
-        if ((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >= 0x7f800000u) {
-            v_top = 0.f;
+                for (int q = 0; q < QN; ++q)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float w = fabsf(vs[q][e]);
-                    v_top = w <= FLT_MAX ? fmaxf(v_top, w) : v_top;
-                }
-            v_top = column_max(v_top);
-        }
-        const int e_new = max((int)((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >> 23) - 127, E);
-        const float v_norm = ldexpf(1.f, kTop - e_new);
-        if (e_new != E) {
-            const float f = ldexpf(1.f, E - e_new);
-#pragma unroll
-            for (int x = 0; x < NQ; ++x)
-#pragma unroll
-                for (int i = 0; i < M; ++i) o[x][i] *= f;
-            E = e_new;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) vs[q] *= v_norm;
+                    for (int e = 0; e < 4; ++e) put(x, q, e, inside(T * q + e, lo[x], hi[x]) ? s(x, q, e) : -INFINITY);
+            }
+        float top[NQ];
+        bool far = false;
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
+            float t[QN];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < QN; ++q) t[q] = fmaxf(fmaxf(s(x, q, 0), s(x, q, 1)), fmaxf(s(x, q, 2), s(x, q, 3)));
+            top[x] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            if (QN == 8) top[x] = fmaxf(top[x], fmaxf(fmaxf(t[QN - 4], t[QN - 3]), fmaxf(t[QN - 2], t[QN - 1])));
+            far |= top[x] > limit[x];
+        }
+        // the exponent moves where a row's first token is seen, and where one has passed it by more than the slack
+        if (__any(far))
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[x][q][e] *= ks[q][e];
-                    if constexpr (!I8) s[x][q][e] = __builtin_fmaf(kl[q][e], qsum[x], s[x][q][e]);
-                }
-            // tokens of the block that the lane's row sees, from its own first
-            int lo = 0, hi = kTile;
-            if (masked) {
-                lo = (int)min(max((int64_t)see_lo[x] - t0, (int64_t)0), (int64_t)kTile) - 4 * j;
-                hi = (paged ? (int)min(max((int64_t)see_hi[x] - t0, (int64_t)0), (int64_t)kTile) : 0) - 4 * j;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[x][q][e] = inside(16 * q + e, lo, hi) ? s[x][q][e] : -INFINITY;
-            }
-            float top = m[x];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[x][q][e]);
-            // the maximum moves where a row's first token is seen, and where it has grown by more than the slack
-            const bool far = m[x] == -INFINITY ? top != -INFINITY : __builtin_fmaf(top, c[x], -mc[x]) > kSlack;
-            if (__any(far)) {
-                top = column_max(top);
-                const float ref = top == -INFINITY ? 0.f : top * c[x];
-                const float alpha = m[x] == -INFINITY ? 0.f : exp2_fast(mc[x] - ref);
+            for (int x = 0; x < NQ; ++x) {
+                const float t = S::max_of(top[x]);
+                const bool none = limit[x] == -INFINITY;
+                const float to = t == -INFINITY ? mc[x] : mc[x] + (none ? t : fmaxf(t, 0.f));
+                const float by = to - mc[x], alpha = none ? 0.f : exp2_fast(-by);
+                mc[x] = to;
+                limit[x] = t == -INFINITY ? limit[x] : kSlack;
                 l[x] *= alpha;
                 bias[x] *= alpha;
+                scale_sums(x, alpha);
 #pragma unroll
-                for (int i = 0; i < M; ++i) o[x][i] *= alpha;
-                m[x] = top;
-                mc[x] = ref;
+                for (int q = 0; q < QN; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) put(x, q, e, s(x, q, e) - by);
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+        for (int x = 0; x < NQ; ++x) {
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < QN; ++q)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float p = exp2_fast(__builtin_fmaf(s[x][q][e], c[x], -mc[x]));
-                    l[x] += p;
-                    s[x][q][e] = p;
+                    const float p = exp2_fast(s(x, q, e));
+                    put(x, q, e, p);
+                    sum[e % 2] += p;
                 }
-            // a token that is not seen has p = 0, and counts for nothing even where its scale is no number
-            if constexpr (!I8) {
-                if (masked) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            bias[x] += inside(16 * q + e, lo, hi) ? s[x][q][e] * vl[q][e] : 0.f;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) bias[x] = __builtin_fmaf(s[x][q][e], vl[q][e], bias[x]);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][q][e] *= vs[q][e];
-            if (masked)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[x][q][e] = inside(16 * q + e, lo, hi) ? s[x][q][e] : 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pf[x][e / 8][e % 8] = (_Float16)s[x][e / 4][C::order(e % 4)];
+            l[x] += sum[0] + sum[1];
         }
+        // a token that is not seen has p = 0, and counts for nothing even where its scale is no number
+        if (masked) {
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                const f4 vq = vs(q), lq = I8 ? f4{} : vl(q);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool seen = inside(T * q + e, lo[x], hi[x]);
+                        if constexpr (!I8) bias[x] += seen ? s(x, q, e) * lq[e] : 0.f;
+                        put(x, q, e, seen ? s(x, q, e) * vq[e] : 0.f);
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                const f4 vq = vs(q), lq = I8 ? f4{} : vl(q);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (!I8) bias[x] = __builtin_fmaf(s(x, q, e), lq[e], bias[x]);
+                        put(x, q, e, s(x, q, e) * vq[e]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+            for (int u = 0; u < PU; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pf[x][u][e] = (_Float16)s(x, 2 * u + e / 4, C::order(e % 4));
     }
 };
 
@@ -495,12 +614,17 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
     __shared__ int e_s[W];
 
     const int kvh = blockIdx.x % a.kv.heads, number = blockIdx.x / a.kv.heads;
-    Piece pc = {number, 0, 0, 1, 0};
-    if (a.share > 0 && !find_piece(a, ROWS, number, pc)) return;
+    Piece pc = {a.share > 0 ? 0 : a.kv.count * a.tiles - 1 - number, 0, 1, 0, 0, 0, 0};   // whole items: the last tiles, the longest, first
+    if (a.share > 0) {
+        const bool found = find_piece(a, ROWS, number, pc);
+        if (number == 0 && kvh == 0 && threadIdx.x == 0) a.cuts[0] = int4{pc.cuts, 0, 0, 0};
+        if (!found) return;
+        if (pc.count > 1 && pc.piece == 0 && kvh == 0 && threadIdx.x == 0)
+            a.cuts[1 + pc.cut] = int4{pc.item, pc.slot, pc.count, 0};
+    }
     const int item = __builtin_amdgcn_readfirstlane(pc.item), b = item / a.tiles;
     const Span t = attn_span(a, b, item % a.tiles, ROWS);
     if (t.nr <= 0) return;
-    if (a.share > 0 && pc.piece == 0 && kvh == 0 && threadIdx.x == 0) a.parts[item] = int2{pc.first, pc.count};
     const int begin = __builtin_amdgcn_readfirstlane(t.first + pc.piece * pc.size);
     const int end = __builtin_amdgcn_readfirstlane(pc.count > 1 ? min(begin + pc.size, t.end) : t.end);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -513,8 +637,8 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
         return blk < end ? kv_page(a.kv, b, blk) : -1;
     };
     int pages = pages_of(0);
-    Rows<FMT, D, BF16, NQ> w;
-    w.load(a, t.s, kvh, t.r0, t.nr, lane);
+    Rows<FMT, D, BF16, 16, NQ, false> w;
+    w.load(a, t.s, kvh, t.r0, t.nr, lane, [](int &, int &) {});
 
     const int page_size = 1 << a.kv.page_shift;
     BlockRegs<FMT, D> r;
@@ -553,10 +677,40 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
                 }
         }
         const int64_t t0 = (int64_t)blk * kTile;
+        // some row does not see all of the block
         const bool masked = page < 0 || blk < (t.seen_lo + kTile - 1) / kTile || blk >= t.seen_hi / kTile;
+        if (masked) {
+            // tokens that no row sees: their scales do not count
+            const int lo = (int)max((int64_t)0, t.lo - t0), hi = page < 0 ? 0 : (int)min((int64_t)kTile, t.hi - t0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    r.vs[q][e] = inside(16 * q + 4 * j + e, lo, hi) ? r.vs[q][e] : 0.f;
+        }
+        // value scales: the largest exponent so far, infinities and NaN aside
+        float v_top = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)       // as fmaxf would, without quieting what was loaded first
+                asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(v_top) : "v"(r.vs[q][e]), "v"(r.vs[q][e + 1]));
+        v_top = column_max(v_top);
+        if ((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >= 0x7f800000u) {
+            v_top = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v_top = finite_max(v_top, r.vs[q][e]);
+            v_top = column_max(v_top);
+        }
+        w.move_to(max((int)((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >> 23) - 127, w.E));
+        const float norm = ldexpf(1.f, kTop - w.E);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) r.vs[q] *= norm;
         h8 pf[NQ][2];
-        w.weigh(s, r.ks, r.kl, r.vs, r.vl, masked, page >= 0, t0, (int)max((int64_t)0, t.lo - t0),
-                page < 0 ? 0 : (int)min((int64_t)kTile, t.hi - t0), j, pf);
+        auto of = [](const f4 *v) { return [v](int q) { return v[q]; }; };
+        w.weigh(s, of(r.ks), of(r.kl), of(r.vs), of(r.vl), masked, page >= 0, t0, j, pf);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MORE) r.load_arrays(part, next_at, j, page_size);
         __builtin_amdgcn_sched_barrier(0);
@@ -630,275 +784,374 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] += ldexpf(ow[e] * g, e_s[q]) + b_s[q][row] * g;
                 }
-                put_result<D, BF16>(a, t, pc.count, number, kvh, ROWS, rr, d0 + d, v, top, sum);
+                put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, rr, d0 + d, v, top, sum);
             }
         }
     }
 }
 
-// Many rows: a workgroup of W waves has 16 * NQ rows of an item in each, and takes the blocks of its piece one by one.
+// Many rows: a workgroup of eight waves has 16 * NQ rows of an item in each, and takes the blocks of its piece one by one.
 // Codes become fp16 operands once for all waves and lie in LDS in the order in which a wave reads them, 16 bytes a lane:
-// no bank conflicts, and no permutation.  Two buffers and one barrier a block: a block is unpacked while the one before is
-// worked on, and the codes of the one after are on their way.
-template <int FMT, int D, bool BF16, int NQ, int W>
-__global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attention_tile_kernel(AttnArgs a)
+// no bank conflicts, and no permutation.
+//
+// A block is two phases of a wave: M, the products (of the block's keys, and of the values of the block before) and the
+// unpacking of what comes next, and S, the softmax.  One is bound by the matrix cores and the LDS, the other by the vector
+// units, and a SIMD has two of the waves: the second four run one phase behind the first, so that each SIMD has one wave in
+// either.  A barrier ends a phase.  With phases counted from 0, the first waves are in M(i) at 2 i and in S(i) at 2 i + 1,
+// the others one later; both write the keys of block i + 1 and the values of block i in M(i), which are read in M(i + 1),
+// from 2 i + 2 on, and lie where those of i - 1 and i - 2 did, last read in M(i - 1), at 2 i - 1.  Scales of block i + 1 go
+// along with its keys and are read in S(i + 1), 2 i + 3 and 2 i + 4: they take turns in four places.
+template <int FMT, int D, bool BF16, int COLS, int W>
+__global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attention_tile_kernel(AttnArgs a)
 {
+    typedef Rows<FMT, D, BF16, COLS, 1, true> R;
+    typedef typename R::S Sh;
     constexpr bool I8 = FMT == LOWBIT_KV_I8;
-    constexpr int ROWS = 16 * NQ * W, KS = D / 32, M = D / 16, A = I8 ? 1 : 2;
+    constexpr int ROWS = COLS * W, KS = R::KS, M = R::M, PU = R::PU, QN = R::QN, A = I8 ? 1 : 2;
     typedef Codes<FMT, D> C;
-    constexpr int CHUNKS = 2 * C::N, MINE = (CHUNKS + W - 1) / W;
-    constexpr int KFRAGS = 4 * KS, FRAGS = KFRAGS + 2 * M;        // 1 KiB each
+    constexpr int MINE = (C::N + W - 1) / W;                      // KiB of codes of keys (and of values) that a wave unpacks
+    constexpr int FRAGS = Sh::TILES * KS;                         // operands of a block's keys (and of its values), 1 KiB each
+    static_assert(FRAGS == M * PU, "as many operands of keys as of values");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    h8 *frags = reinterpret_cast<h8 *>(lds);                      // [2][FRAGS][64]
-    float *arrays = reinterpret_cast<float *>(lds + 2 * FRAGS * 1024);   // [2][K, V][scale, minimum][64]
+    h8 *kfrag = reinterpret_cast<h8 *>(lds), *vfrag = kfrag + 2 * FRAGS * 64;   // [2][FRAGS][64] each
+    float *arrays = reinterpret_cast<float *>(vfrag + 2 * FRAGS * 64);          // [4][K, V][scale, minimum][64]
 
     const int kvh = blockIdx.x % a.kv.heads, number = blockIdx.x / a.kv.heads;
-    Piece pc = {number, 0, 0, 1, 0};
-    if (a.share > 0 && !find_piece(a, ROWS, number, pc)) return;
+    Piece pc = {a.share > 0 ? 0 : a.kv.count * a.tiles - 1 - number, 0, 1, 0, 0, 0, 0};   // whole items: the last tiles, the longest, first
+    if (a.share > 0) {
+        const bool found = find_piece(a, ROWS, number, pc);
+        if (number == 0 && kvh == 0 && threadIdx.x == 0) a.cuts[0] = int4{pc.cuts, 0, 0, 0};
+        if (!found) return;
+        if (pc.count > 1 && pc.piece == 0 && kvh == 0 && threadIdx.x == 0)
+            a.cuts[1 + pc.cut] = int4{pc.item, pc.slot, pc.count, 0};
+    }
     const int item = __builtin_amdgcn_readfirstlane(pc.item), b = item / a.tiles;
     const Span t = attn_span(a, b, item % a.tiles, ROWS);
     if (t.nr <= 0) return;
-    if (a.share > 0 && pc.piece == 0 && kvh == 0 && threadIdx.x == 0) a.parts[item] = int2{pc.first, pc.count};
     const int begin = __builtin_amdgcn_readfirstlane(t.first + pc.piece * pc.size);
     const int end = __builtin_amdgcn_readfirstlane(pc.count > 1 ? min(begin + pc.size, t.end) : t.end);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int j = lane >> 4, n = lane & 15;
+    const int j = lane / COLS, n = lane % COLS;
     const int page_size = 1 << a.kv.page_shift;
     // the wave's own rows, and what they see
-    const int w0 = wave * 16 * NQ, wn = min(t.nr - w0, 16 * NQ);
+    const int w0 = wave * COLS, wn = min(t.nr - w0, COLS);
     const Span ws = attn_rows(a, t.s, t.r0 + w0, wn);
 
     auto pages_of = [&](int blk) { return blk + lane < end ? kv_page(a.kv, b, blk + lane) : -1; };
     int pages = pages_of(begin);
-    Rows<FMT, D, BF16, NQ> w;
-    w.load(a, t.s, kvh, wn > 0 ? t.r0 + w0 : t.r0, wn, lane);
+    R w;
+    const float k_factor = w.load(a, t.s, kvh, wn > 0 ? t.r0 + w0 : t.r0, wn, lane, [&](int &hi, int &lo) {
+        int *m = reinterpret_cast<int *>(lds);
+        for (int o = 32; o > 0; o >>= 1) {
+            hi = max(hi, __shfl_xor(hi, o));
+            lo = min(lo, __shfl_xor(lo, o));
+        }
+        if (lane == 0) {
+            m[wave] = hi;
+            m[W + wave] = lo;
+        }
+        __syncthreads();
+        for (int q = 0; q < W; ++q) {
+            hi = max(hi, m[q]);
+            lo = min(lo, m[W + q]);
+        }
+        hi = __builtin_amdgcn_readfirstlane(hi);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        __syncthreads();
+    });
     uint32_t mant = 0x64006400u;
     asm("" : "+v"(mant));
 
-    // codes and scales of a block on their way to LDS
-    u4 raw[MINE];
-    float scale = 0.f, low = 0.f;
-    int page_in = -1;                    // page of the block in raw
-    auto fetch = [&](int blk) {
-        const int i = blk - begin;
+    // Codes on their way to LDS: keys of a block, values of the one before.  Past the last block its loads are repeated, so
+    // that nothing in phase M hangs on a branch.
+    u4 kraw[MINE], vraw[MINE];
+    int page_k = -1;                     // page of the keys in kraw
+    auto part_of = [&](int page) { return buffer_rsrc(kv_part(a.kv, max(page, 0), kvh), a.kv.part); };
+    auto in_page = [&](int blk) { return (blk * kTile) & (page_size - 1); };
+    auto fetch = [&](int blk) {          // the keys of blk, the values of the block before
+        const int i = blk - begin, page_v = page_k;
         if ((i & 63) == 0 && i > 0) pages = pages_of(blk);
-        page_in = __builtin_amdgcn_readlane(pages, i & 63);
-        const auto part = buffer_rsrc(kv_part(a.kv, max(page_in, 0), kvh), a.kv.part);
-        const int at = (blk * kTile) & (page_size - 1);
+        page_k = blk < end ? __builtin_amdgcn_readlane(pages, i & 63) : page_k;
+        const auto pk = part_of(page_k), pv = part_of(page_v);
+        const int at_k = kv_code_bytes(FMT, in_page(min(blk, end - 1)), D);
+        const int at_v = kv_code_bytes(FMT, page_size + in_page(max(blk - 1, begin)), D);
 #pragma unroll
         for (int q = 0; q < MINE; ++q) {
             const int chunk = wave + q * W;
-            const int from = chunk < C::N ? kv_code_bytes(FMT, at, D) + chunk * 1024
-                                          : kv_code_bytes(FMT, page_size + at, D) + (chunk - C::N) * 1024;
-            if (chunk < CHUNKS) raw[q] = BlockRegs<FMT, D>::get(part, lane * 16, from);
+            if (C::N % W != 0 && chunk >= C::N) break;
+            kraw[q] = BlockRegs<FMT, D>::get(pk, lane * 16, at_k + chunk * 1024);
+            vraw[q] = BlockRegs<FMT, D>::get(pv, lane * 16, at_v + chunk * 1024);
         }
-        if (wave < 2) {
-            const int from = 2 * kv_code_bytes(FMT, page_size, D) + at * 4 + wave * A * page_size * 4;
-            scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part, lane * 4, from, 0));
+    };
+    // The operands that a wave unpacks, one by one: OPS / 2 of the keys of the piece's block i + 1, then as many of the values
+    // of block i.  A KiB of codes holds 2 operands of 8 bits, 4 of 4 bits: of keys, two steps of 64 dims (of 16 tokens each);
+    // of values, two steps of 32 tokens (of 16 dims each).
+    constexpr int PER = I8 ? 2 : 4, OPS = 2 * MINE * PER;
+    auto unpack = [&](int op, int i) {
+        const int q = op / PER % MINE, v = op % PER, chunk = wave + q * W;
+        if (C::N % W != 0 && chunk >= C::N) return;
+        const int sj = lane >> 4, sr = lane & 15;        // the page's lane: 16 bytes of dims 16 sj of token sr, tokens 4 sj of dim sr
+        if (op < OPS / 2) {
+            const h8 f = C::key_of(kraw[q], v, mant);
+            const int d = chunk % (D / 64), q0 = chunk / (D / 64) * (PER / 2) + v / 2;   // 64 dims, 16 tokens
+            h8 *to = kfrag + (i + 1 & 1) * FRAGS * 64;
+            if constexpr (COLS == 16) to[(q0 * KS + 2 * d + v % 2) * 64 + lane] = f;
+            else to[(q0 / 2 * KS + 4 * d + sj) * 64 + v % 2 * 32 + q0 % 2 * 16 + sr] = f;
+        } else {
+            const h8 f = C::value_of(vraw[q], v / 2, v % 2, mant);
+            const int d = chunk * (PER / 2) + v / 2;                                     // 16 dims
+            h8 *to = vfrag + (i & 1) * FRAGS * 64;
+            if constexpr (COLS == 16) to[(d * 2 + v % 2) * 64 + lane] = f;
+            else
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    reinterpret_cast<h4 *>(to + (d / 2 * 4 + v % 2 * 2 + u) * 64 + sj % 2 * 32 + d % 2 * 16 + sr)[sj / 2] =
+                        h4{f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]};
+        }
+    };
+    // Scales of a block on their way to LDS, a token a lane.  Every wave has all of them: the largest exponent of the value
+    // scales so far (of tokens that some row sees, infinities and NaN aside) is the same in each, and comes about in steps
+    // that fit between products.
+    float scale[2], low[2], v_top;
+    int v_exp = -100, page_a = -1;
+    auto fetch_scales = [&](int blk) {   // of blk, whose page is page_k
+        page_a = page_k;
+        const auto part = part_of(page_k);
+        const int from = 2 * kv_code_bytes(FMT, page_size, D) + in_page(min(blk, end - 1)) * 4;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            scale[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part, lane * 4, from + v * A * page_size * 4, 0));
             if constexpr (!I8)
-                low = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part, lane * 4, from + page_size * 4, 0));
+                low[v] = __uint_as_float(
+                    __builtin_amdgcn_raw_buffer_load_b32(part, lane * 4, from + (v * A + 1) * page_size * 4, 0));
         }
     };
-    auto unpack = [&](int buf) {
-        h8 *to = frags + buf * FRAGS * 64 + lane;
-#pragma unroll
-        for (int q = 0; q < MINE; ++q) {
-            const int chunk = wave + q * W;
-            if (chunk >= CHUNKS) break;
-            if (chunk < C::N) {
-                // keys: for 8 bits 16 tokens' 64 dims, two steps; for 4 bits those of 32 tokens
-                const int i = chunk % (D / 64), q0 = chunk / (D / 64) * (I8 ? 1 : 2);
-#pragma unroll
-                for (int v = 0; v < (I8 ? 2 : 4); ++v)
-                    to[((q0 + v / 2) * KS + 2 * i + v % 2) * 64] = C::key_of(raw[q], v, mant);
-            } else {
-                // values: 16 (32) dims, two steps of 32 tokens
-                const int i = (chunk - C::N) * (I8 ? 1 : 2);
-#pragma unroll
-                for (int v = 0; v < (I8 ? 2 : 4); ++v)
-                    to[(KFRAGS + (i + v / 2) * 2 + v % 2) * 64] = C::value_of(raw[q], v / 2, v % 2, mant);
-            }
+    constexpr int kScaleSteps = 8;
+    auto unpack_scales = [&](int step, int i) {
+        if (step == 0) {
+            const int64_t token = (int64_t)(begin + i) * kTile + lane;
+            v_top = ((token >= t.lo) & (token < t.hi) & (page_a >= 0)) ? finite_max(0.f, scale[1]) : 0.f;
         }
-        if (wave < 2) {
-            float *at = arrays + ((buf * 2 + wave) * A) * 64 + lane;
-            at[0] = scale;
-            if constexpr (!I8) at[64] = __builtin_fmaf(8.f, scale, low);
+        if (step == 1) v_top = dpp_max<0xb1>(v_top);
+        if (step == 2) v_top = dpp_max<0x4e>(v_top);
+        if (step == 3) v_top = dpp_max<0x141>(v_top);
+        if (step == 4) v_top = dpp_max<0x140>(v_top);
+        if (step == 5) v_top = column_max(v_top);
+        if (step == 6)
+            v_exp = max(v_exp, (int)((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >> 23) - 127);
+        if (step == 7) {
+            float *at = arrays + (i & 3) * 2 * A * 64 + lane;
+            if (wave == 0) {
+                at[0] = scale[0] * k_factor;
+                if constexpr (!I8) at[64] = __builtin_fmaf(8.f, scale[0], low[0]) * k_factor;
+            }
+            if (wave == 1) {
+                at[A * 64] = ldexpf(scale[1], kTop - v_exp);
+                if constexpr (!I8) at[3 * 64] = __builtin_fmaf(8.f, scale[1], low[1]);
+            }
         }
     };
 
-    int page_next = -1;
-    if (begin < end) {
+    const int count = end - begin;
+    typename R::Acc s[1][Sh::TILES];
+    h8 pf[1][PU];
+    auto no_weights = [&] {
+#pragma unroll
+        for (int u = 0; u < PU; ++u) pf[0][u] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+    };
+    no_weights();
+    // Products of the values of block i - 1, then of the keys of block i; kAhead operands are under way from LDS, and the
+    // unpacking goes in between: the matrix cores leave the vector unit three of four of its turns.
+    constexpr int kAhead = 6;
+    auto multiply = [&](auto keys, int i) {
+        constexpr bool KEYS = decltype(keys)::value;
+        constexpr int ALL = KEYS ? 2 * FRAGS : FRAGS;
+        const h8 *vf = vfrag + (i - 1 & 1) * FRAGS * 64 + lane, *kf = kfrag + (i & 1) * FRAGS * 64 + lane;
+        h8 ring[kAhead];
+        auto ask = [&](int q) { ring[q % kAhead] = q < FRAGS ? vf[q * 64] : kf[(q - FRAGS) * 64]; };
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) ask(q);
+#pragma unroll
+        for (int q = 0; q < FRAGS; ++q) {
+            const h8 f = ring[q % kAhead];
+            w.o[0][q / PU] = Sh::mul(f, pf[0][q % PU], w.o[0][q / PU]);
+            if (q + kAhead < ALL) ask(q + kAhead);
+            if (KEYS)
+#pragma unroll
+                for (int op = 0; op < OPS; ++op)
+                    if (q == op * FRAGS / OPS) unpack(op, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!KEYS) return;
+        fetch(begin + i + 2);
+#pragma unroll
+        for (int q = 0; q < FRAGS; ++q) {
+            const h8 f = ring[(FRAGS + q) % kAhead];
+            const int t = q / KS, k = q % KS;
+            s[0][t] = Sh::mul(f, w.qf[0][k], k == 0 ? typename R::Acc{} : s[0][t]);
+            if (FRAGS + q + kAhead < ALL) ask(FRAGS + q + kAhead);
+#pragma unroll
+            for (int step = 0; step < kScaleSteps; ++step)
+                if (q == step * FRAGS / kScaleSteps) unpack_scales(step, i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        fetch_scales(begin + i + 2);
+    };
+    if (count > 0) {
         fetch(begin);
-        unpack(0);
-        page_next = page_in;
-        if (begin + 1 < end) fetch(begin + 1);
-    }
-    for (int blk = begin; blk < end; ++blk) {
-        const int buf = (blk - begin) & 1, page = page_next;
+        int page_next = page_k;          // of block i + 1
+        fetch_scales(begin);
+#pragma unroll
+        for (int op = 0; op < OPS / 2; ++op) unpack(op, -1);
+#pragma unroll
+        for (int step = 0; step < kScaleSteps; ++step) unpack_scales(step, 0);
+        fetch(begin + 1);                // keys of block 1, values of block 0
+        fetch_scales(begin + 1);
         __syncthreads();
-        if (blk + 1 < end) {
-            unpack(buf ^ 1);
-            page_next = page_in;
-            if (blk + 2 < end) fetch(blk + 2);
-        }
-        if (wn <= 0 || blk < ws.first || blk >= ws.end || page < 0) continue;     // none of the wave's rows sees it
-        const h8 *f = frags + buf * FRAGS * 64 + lane;
-        f4 s[NQ][4];
+        for (int i = 0; i < count; ++i) {
+            // M
+            const int page = page_next, e_now = v_exp, blk = begin + i;
+            page_next = page_k;
+            __builtin_amdgcn_s_setprio(1);
+            multiply(std::true_type{}, i);
+            if (i == 0) w.clear();                       // no values were there yet
+            // the keys' scales before the barrier, the others as they are needed
+            const float *ar = arrays + (i & 3) * 2 * A * 64 + 4 * j;
+            auto get = [ar](int which) { return [=](int q) { return *reinterpret_cast<const f4 *>(ar + which * 64 + 64 / QN * q); }; };
+            f4 ks[QN];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) s[x][q] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const h8 kf = f[(q * KS + k) * 64];
-#pragma unroll
-                for (int x = 0; x < NQ; ++x)
-                    s[x][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, w.qf[x][k], s[x][q], 0, 0, 0);
+            for (int q = 0; q < QN; ++q) ks[q] = get(0)(q);
+            __builtin_amdgcn_s_setprio(0);
+            __syncthreads();
+            // S
+            if (wn > 0 && blk >= ws.first && blk < ws.end && page >= 0) {
+                const bool masked = blk < (ws.seen_lo + kTile - 1) / kTile || blk >= ws.seen_hi / kTile;
+                w.move_to(e_now);
+                w.weigh(s, [&](int q) { return ks[q]; }, get(1), get(A), get(3), masked, true, (int64_t)blk * kTile, j, pf);
+            } else {
+                no_weights();
             }
         }
-        f4 ks[4], vs[4], kl[4], vl[4];
-        const float *ar = arrays + buf * 2 * A * 64 + 4 * j;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            ks[q] = *reinterpret_cast<const f4 *>(ar + 16 * q);
-            vs[q] = *reinterpret_cast<const f4 *>(ar + A * 64 + 16 * q);
-            if constexpr (!I8) {
-                kl[q] = *reinterpret_cast<const f4 *>(ar + 64 + 16 * q);
-                vl[q] = *reinterpret_cast<const f4 *>(ar + 3 * 64 + 16 * q);
-            }
-        }
-        const int64_t t0 = (int64_t)blk * kTile;
-        const bool masked = blk < (ws.seen_lo + kTile - 1) / kTile || blk >= ws.seen_hi / kTile;
-        h8 pf[NQ][2];
-        w.weigh(s, ks, kl, vs, vl, masked, true, t0, (int)max((int64_t)0, ws.lo - t0),
-                (int)min((int64_t)kTile, ws.hi - t0), j, pf);
-#pragma unroll
-        for (int i = 0; i < M; ++i)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const h8 vf = f[(KFRAGS + i * 2 + u) * 64];
-#pragma unroll
-                for (int x = 0; x < NQ; ++x)
-                    w.o[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[x][u], w.o[x][i], 0, 0, 0);
-            }
+        multiply(std::false_type{}, count);              // the values of the last block
     }
 
+    const float sum = Sh::sum_of(w.l[0]), low_sum = Sh::sum_of(w.bias[0]);
+    if (n >= wn) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum, add = low_sum * inv;
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        w.l[x] = column_sum(w.l[x]);
-        w.bias[x] = column_sum(w.bias[x]);
-        if (x * 16 + n >= wn) continue;
-        const float inv = w.l[x] == 0.f ? 0.f : 1.f / w.l[x], add = w.bias[x] * inv;
+    for (int i = 0; i < M; ++i)
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
+        for (int q = 0; q < R::EL / 4; ++q) {
             f4 v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = ldexpf(w.o[x][i][e] * inv, w.E - kTop) + add;
-            put_result<D, BF16>(a, t, pc.count, number, kvh, ROWS, w0 + x * 16 + n, 16 * i + 4 * j, v, w.mc[x], w.l[x]);
+            for (int e = 0; e < 4; ++e) v[e] = ldexpf(w.o[0][i][4 * q + e] * inv, w.E - kTop) + add;
+            put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, w0 + n, COLS * i + 8 * q + 4 * j, v, w.mc[0], sum);
         }
-    }
 }
 
-// The pieces of a row joined: each has its own normalised result, and weighs sum * 2^maximum.  A workgroup takes one row
-// of one head, dim / 4 lanes for each of its pieces, 256 / (dim / 4) pieces at a time.
+// The pieces of a cut item's rows joined: each has its own normalised result, and weighs sum * 2^maximum.  A workgroup takes
+// `per` rows of one head one by one, dim / 4 lanes for each of the row's pieces, 256 / (dim / 4) pieces at a time.
 template <int D, bool BF16>
-__global__ __launch_bounds__(256) void kv_attention_join_kernel(AttnArgs a, int rows, int most)
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(AttnArgs a, int rows, int per, int groups)
 {
     constexpr int LANES = D / 4, G = 256 / LANES;
     __shared__ f4 part[G][LANES];
     __shared__ float sums[G];
-    const int rr = blockIdx.x % most, kvh = blockIdx.x / most % a.kv.heads, item = blockIdx.x / most / a.kv.heads;
-    const Span t = attn_span(a, item / a.tiles, item % a.tiles, rows);
-    if (rr >= t.nr) return;
-    const int2 pc = a.parts[item];                    // first piece, pieces
-    if (pc.y <= 1) return;
-    const int64_t step = (int64_t)a.kv.heads * rows, first = ((int64_t)pc.x * a.kv.heads + kvh) * rows + rr;
+    const int kvh = blockIdx.x % a.kv.heads, r0 = blockIdx.x / a.kv.heads % groups * per;
+    const int cut = blockIdx.x / a.kv.heads / groups;
+    const int4 it = a.cuts[1 + cut];
+    if (cut >= a.cuts[0].x) return;
+    const Span t = attn_span(a, it.x / a.tiles, it.x % a.tiles, rows);
+    const int64_t step = (int64_t)a.kv.heads * rows;
     const int lane = threadIdx.x & 63, g = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
-    float top = -INFINITY;
-    for (int i = lane; i < pc.y; i += 64) {
-        const float2 ml = a.part_ml[first + i * step];
-        if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
+    for (int rr = r0; rr < min(r0 + per, t.nr); ++rr) {
+        const int64_t first = ((int64_t)it.y * a.kv.heads + kvh) * rows + rr;
+        float top = -INFINITY;
+        for (int i = lane; i < it.z; i += 64) {
+            const float2 ml = a.part_ml[first + i * step];
+            if (ml.y != 0.f) top = fmaxf(top, ml.x);
+        }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    f4 v = {0.f, 0.f, 0.f, 0.f};
-    float sum = 0.f;
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        f4 v = {0.f, 0.f, 0.f, 0.f};
+        float sum = 0.f;
 #pragma unroll 4
-    for (int i = g; i < pc.y; i += G) {
-        const float2 ml = a.part_ml[first + i * step];
-        const f4 o = *reinterpret_cast<const f4 *>(a.part_o + (first + i * step) * D + d);
-        const float f = ml.y == 0.f ? 0.f : ml.y * exp2_fast(ml.x - top);
-        sum += f;
-        v += o * f;
-    }
-    part[g][threadIdx.x % LANES] = v;
-    if (d == 0) sums[g] = sum;
-    __syncthreads();
-    if (threadIdx.x >= LANES) return;
-    v = f4{0.f, 0.f, 0.f, 0.f};
-    sum = 0.f;
+        for (int i = g; i < it.z; i += G) {
+            const float2 ml = a.part_ml[first + i * step];
+            const f4 o = *reinterpret_cast<const f4 *>(a.part_o + (first + i * step) * D + d);
+            const float f = ml.y == 0.f ? 0.f : ml.y * exp2_fast(ml.x - top);
+            sum += f;
+            v += o * f;
+        }
+        if (rr > r0) __syncthreads();                 // the row before is read
+        part[g][threadIdx.x % LANES] = v;
+        if (d == 0) sums[g] = sum;
+        __syncthreads();
+        if (threadIdx.x >= LANES) continue;
+        v = f4{0.f, 0.f, 0.f, 0.f};
+        sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-        v += part[i][threadIdx.x];
-        sum += sums[i];
+        for (int i = 0; i < G; ++i) {
+            v += part[i][threadIdx.x];
+            sum += sums[i];
+        }
+        put_result<D, BF16>(a, t, 1, 0, kvh, rows, rr, d, v * (sum == 0.f ? 0.f : 1.f / sum), 0.f, 0.f);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int r = t.r0 + rr, i = r / a.group, h = r % a.group;
-    uint16_t *to = a.y + ((int64_t)(t.s.row0 + i) * a.q_heads + kvh * a.group + h) * D + d;
-    const ushort4 w4 = {round_out<BF16>(v[0] * inv), round_out<BF16>(v[1] * inv), round_out<BF16>(v[2] * inv),
-                        round_out<BF16>(v[3] * inv)};
-    *reinterpret_cast<ushort4 *>(to) = w4;
 }
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;                // of a workgroup with few rows
+constexpr int kTileRows = 128;
+constexpr int kWholeBlocks = 16;         // blocks up to which an item is not worth a second launch
+constexpr int64_t kFewBeside = 16;       // rows of a sequence up to which it goes with the few, where others have many
 
 // A launch over the sequences of over < rows * group <= upto
 struct AttnPlan {
     bool tile;
-    int nq, waves, rows;                 // 16 * nq rows for all waves (few) or for each (tile)
-    int64_t over, upto, pieces;          // workgroups for each head
-    int tiles, share;
+    int nq, rows;                        // rows of an item: 16 * nq for all waves (few), kTileRows (tile)
+    int64_t over, upto, pieces, slots;   // workgroups for each head at most, results of pieces
+    int tiles, share, cuts;              // cuts: items that are cut, at most
 };
 int64_t plan_bytes(const AttnPlan &p, const KvArgs &a)
 {
     if (p.share == 0) return 0;
-    return p.pieces * a.heads * p.rows * (a.dim * 4 + 8) + round_up((int64_t)p.tiles * a.count * 8, 256);
+    return p.slots * a.heads * p.rows * (a.dim * 4 + 8) + ((int64_t)p.cuts + 1) * (int64_t)sizeof(int4);
 }
-void cut_plan(AttnPlan &p, const KvArgs &a, int64_t most_rows, int slots, int min_piece)
+void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int resident)
 {
     p.tiles = (int)((most_rows + p.rows - 1) / p.rows);
     const int64_t items = (int64_t)p.tiles * a.count, blocks = ((int64_t)a.width << a.page_shift) / kTile;
-    const bool cut = items * a.heads < slots * (p.tile ? 1 : 4) && items <= 1024 && blocks > min_piece;
-    p.share = cut ? std::max(slots / a.heads, 1) : 0;
-    p.pieces = cut ? std::min(items + p.share, items * ((blocks + min_piece - 1) / min_piece)) : items;
+    const bool cut = items <= kMaxItems && blocks > kWholeBlocks;
+    p.share = cut ? std::max(resident / a.heads, 1) : 0;
+    // tiles that there can be: whole ones of all rows, and a sequence's last
+    const int64_t there = std::min(items, (int64_t)a.rows * group / p.rows + std::min(a.count, a.rows));
+    p.pieces = cut ? there + p.share : items;
+    p.slots = 2 * p.share;                                   // a cut item has two pieces or more
+    p.cuts = (int)std::min<int64_t>(there, p.share);
 }
-constexpr int64_t kFewRows = 32, kFewBeside = 16;
 // one launch or two: sequences of many rows first
 int attn_plan(const KvArgs &a, int q_heads, AttnPlan *p)
 {
-    const int64_t rows = (int64_t)a.max_rows * (q_heads / a.heads);
+    const int group = q_heads / a.heads;
+    const int64_t rows = (int64_t)a.max_rows * group, few = a.dim == 64 ? 64 : a.dim == 128 ? 32 : 16;
     int n = 0;
-    const int64_t few = kFewRows;
     if (rows > few) {
         AttnPlan &t = p[n++];
         t.tile = true;
-        t.nq = a.dim == 256 ? 1 : 2;
-        t.waves = 8;
-        t.rows = 16 * t.nq * t.waves;
+        t.nq = 0;
+        t.rows = kTileRows;
         t.over = a.count > 1 ? kFewBeside : 0;
         t.upto = INT64_MAX;
-        cut_plan(t, a, rows, 256, kMinPiece);
+        cut_plan(t, a, group, rows, a.dim == 256 ? 256 : 512);
         if (a.count == 1) return n;
     }
     AttnPlan &f = p[n++];
-    f.tile = false;
     const int64_t most = rows > few ? kFewBeside : rows;
-    f.nq = most <= 16 ? 1 : 2;
-    f.waves = kWaves;
+    f.tile = false;
+    f.nq = most <= 16 ? 1 : most <= 32 ? 2 : 4;
     f.rows = 16 * f.nq;
     f.over = 0;
     f.upto = rows > few ? kFewBeside : INT64_MAX;
-    cut_plan(f, a, most, a.dim * f.nq > 128 ? 256 : 512, kMinPiece);
+    cut_plan(f, a, group, most, a.dim * f.nq > 128 ? 256 : 512 * 4 / kWaves);
     return n;
 }
 
@@ -938,14 +1191,14 @@ hipError_t launch_kv_attention(const KvArgs &kv, const void *q, int64_t q_stride
                    static_cast<uint16_t *>(y), p.tiles, p.over, p.upto, p.share, nullptr, nullptr, nullptr};
         if (p.share > 0) {
             a.part_o = static_cast<float *>(ws);
-            a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.pieces * kv.heads * p.rows * kv.dim);
-            a.parts = reinterpret_cast<int2 *>(a.part_ml + p.pieces * kv.heads * p.rows);
+            a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.slots * kv.heads * p.rows * kv.dim);
+            a.cuts = reinterpret_cast<int4 *>(a.part_ml + p.slots * kv.heads * p.rows);
         }
         const unsigned grid = (unsigned)(p.pieces * kv.heads);
-        auto tile = [&](auto nq, auto waves) {
-            constexpr int NQ = decltype(nq)::value, W = decltype(waves)::value;
-            constexpr size_t lds = 512 * D + (F == LOWBIT_KV_I8 ? 1024 : 2048);
-            auto kernel = kv_attention_tile_kernel<F, D, B, NQ, W>;
+        auto tile = [&](auto cols, auto waves) {
+            constexpr int COLS = decltype(cols)::value, W = decltype(waves)::value;
+            constexpr size_t lds = 512 * D + (F == LOWBIT_KV_I8 ? 2048 : 4096);
+            auto kernel = kv_attention_tile_kernel<F, D, B, COLS, W>;
             if (lds > 65536) {
                 const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                                          (int)lds);
@@ -956,19 +1209,28 @@ hipError_t launch_kv_attention(const KvArgs &kv, const void *q, int64_t q_stride
         };
         typedef std::integral_constant<int, 1> one;
         typedef std::integral_constant<int, 2> two;
+        typedef std::integral_constant<int, 4> four;
         hipError_t e;
         if (p.tile) {
-            typedef std::integral_constant<int, D == 256 ? 1 : 2> nq;
-            e = p.waves == 8 ? tile(nq{}, std::integral_constant<int, 8>{}) : tile(nq{}, std::integral_constant<int, 4>{});
+            typedef std::integral_constant<int, 16> c16;
+            typedef std::integral_constant<int, 32> c32;
+            typedef std::integral_constant<int, 4> w4;
+            typedef std::integral_constant<int, 8> w8;
+            if constexpr (D == 256) e = tile(c16{}, w8{});
+            else e = tile(c32{}, w4{});
         } else {
-            if (p.nq == 1) kv_attention_kernel<F, D, B, one::value, kWaves><<<grid, kWaves * 64, 0, s>>>(a);
-            else kv_attention_kernel<F, D, B, two::value, kWaves><<<grid, kWaves * 64, 0, s>>>(a);
-            e = hipGetLastError();
+            auto few = [&](auto nq) {
+                kv_attention_kernel<F, D, B, decltype(nq)::value, kWaves><<<grid, kWaves * 64, 0, s>>>(a);
+                return hipGetLastError();
+            };
+            if constexpr (D == 64) e = p.nq == 1 ? few(one{}) : p.nq == 2 ? few(two{}) : few(four{});
+            else if constexpr (D == 128) e = p.nq == 1 ? few(one{}) : few(two{});
+            else e = few(one{});
         }
         if (e != hipSuccess || p.share == 0) return e;
-        const int most = (int)std::min<int64_t>(p.rows, (int64_t)kv.max_rows * a.group);
-        kv_attention_join_kernel<D, B><<<(unsigned)((int64_t)kv.count * p.tiles * kv.heads * most), 256, 0, s>>>(
-            a, p.rows, most);
+        const int per = p.tile ? 4 : 1, most = (int)std::min<int64_t>(p.rows, (int64_t)kv.max_rows * a.group);
+        const int groups = (most + per - 1) / per;
+        kv_attention_join_kernel<D, B><<<(unsigned)((int64_t)p.cuts * kv.heads * groups), 256, 0, s>>>(a, p.rows, per, groups);
         return hipGetLastError();
     };
     auto with_bf = [&](const AttnPlan &p, auto fmt, auto dim) {

@@ -8,11 +8,13 @@
 // step is one binary32 rounding, so equal rows give equal bytes.
 //
 // One workgroup takes 64 tokens of one sequence that lie in one block of a page,
-// for the keys or the values of one head; dim / 8 lanes hold a row, 8 values
-// each.  A row of keys goes to memory in pieces of 8 (4) bytes as it is.  The
-// page holds values by dim, 4 tokens to a dword, so they are turned in LDS, in
-// the page's own byte order, and leave it 16 bytes at a time where the block is
-// whole, by dwords and bytes at its ends: no byte of another token is written.
+// for the keys or the values of one head, and asks for all of its rows at once.
+// A wave holds 4 tokens in lanes 16 apart (8 tokens of 64 dims), 8 or 16 dims to
+// a lane.  Keys go to memory as they are, 8 (4) bytes a lane.  The page holds
+// values by dim, 4 tokens to a dword: four lanes exchange their bytes by swaps of
+// lane rows, the dwords meet in LDS in the page's order, and leave it 16 bytes at
+// a time where the block is whole, by dwords and bytes at its ends: no byte of
+// another token is written.
 #include <cfloat>
 
 #include "kv_cache.hpp"
@@ -63,17 +65,18 @@ __device__ __forceinline__ bool kv_block(const KvArgs &a, int blocks, Block &o)
     return true;
 }
 
-// Byte of (token t, first dim d of 8) in a page's keys, and of (token t, dim d)
-// in a block of values (4 bits: d counts bytes: 16 of every 32 dims)
+// Byte of (token t, first dim d of 8) in a page's keys
 template <int FMT, int D>
 __device__ __forceinline__ int key_byte(int t, int d)
 {
     if (FMT == LOWBIT_KV_I8) return ((t / 16 * (D / 64) + d / 64) * 4 + d % 64 / 16) * 256 + t % 16 * 16 + d % 16;
     return ((t / 32 * (D / 64) + d / 64) * 4 + d % 64 / 16) * 256 + t % 16 * 16 + t % 32 / 16 * 8 + d % 16 / 8 * 4;
 }
-__device__ __forceinline__ int value_byte(int t, int d)
+// Dword of a block of values in LDS: 4 tokens from 4 * quad on, byte b of a token's row (4 bits: 16 of every 32 dims).
+// The page's order but for the last two bits, which are turned by b / 16 so that 64 lanes meet few banks twice.
+__device__ __forceinline__ int value_word(int quad, int b)
 {
-    return (d / 16 * 4 + t % 16 / 4) * 256 + d % 16 * 16 + t / 16 * 4 + t % 4;
+    return (b / 16 * 4 + quad % 4) * 64 + b % 16 * 4 + (quad / 4 ^ (b / 16 & 3));
 }
 
 template <int LANES, typename T, typename F>
@@ -84,94 +87,169 @@ __device__ __forceinline__ T across(T v, F f)
     return v;
 }
 
+// Four tokens in lanes l, l + 16, l + 32, l + 48, with 8 bytes each (a: 0..3, b: 4..7), become 4 tokens of bytes 2 r and
+// 2 r + 1 in the lanes of row r (a, b).  The inverse is turn_back.
+__device__ __forceinline__ void turn(uint32_t &a, uint32_t &b)
+{
+    const auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    const uint32_t x = __builtin_amdgcn_perm(p[1], p[0], 0x05040100u), y = __builtin_amdgcn_perm(p[1], p[0], 0x07060302u);
+    const auto q = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    a = __builtin_amdgcn_perm(q[1], q[0], 0x06020400u);
+    b = __builtin_amdgcn_perm(q[1], q[0], 0x07030501u);
+}
+__device__ __forceinline__ void turn_back(uint32_t &a, uint32_t &b)
+{
+    const uint32_t x = __builtin_amdgcn_perm(b, a, 0x06020400u), y = __builtin_amdgcn_perm(b, a, 0x07030501u);
+    const auto q = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    const uint32_t c = __builtin_amdgcn_perm(q[1], q[0], 0x05040100u), d = __builtin_amdgcn_perm(q[1], q[0], 0x07060302u);
+    const auto p = __builtin_amdgcn_permlane32_swap(c, d, false, false);
+    a = p[0];
+    b = p[1];
+}
+
+// How a workgroup shares out a block: ROUNDS times, a wave takes QUADS times 4 tokens, a lane CH times 8 dims of one.
+template <int D>
+struct Share {
+    static constexpr int LANES = D < 128 ? D / 8 : 16, CH = D / (8 * LANES), QUADS = 16 / LANES;
+    static constexpr int ROUNDS = 16 / (kThreads / 64 * QUADS);
+    int l, t4, wave, first;              // lane of its row, token of its quad; first quad of the block that has rows
+    __device__ __forceinline__ explicit Share(const Block &o)
+    {
+        const int lane = threadIdx.x & 63;
+        l = lane % LANES;
+        t4 = lane / 16;
+        wave = threadIdx.x / 64;
+        first = o.lo / 4 + lane / LANES % QUADS;
+    }
+    __device__ __forceinline__ int quad(int round) const { return first + (round * (kThreads / 64) + wave) * QUADS; }
+    __device__ __forceinline__ int dim(int ch) const { return ch * 128 + l * 8; }
+};
+
 template <int FMT, int D, bool BF16>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, const uint16_t *k, int64_t k_stride,
                                                             const uint16_t *v, int64_t v_stride, int blocks)
 {
     constexpr bool I8 = FMT == LOWBIT_KV_I8;
-    constexpr int LANES = D / 8, STEP = kThreads / LANES, IMAGE = kv_code_bytes(FMT, 64, D);
-    __shared__ __attribute__((aligned(16))) uint8_t image[IMAGE];
+    typedef Share<D> S;
+    constexpr int IMAGE = kv_code_bytes(FMT, 64, D);
+    __shared__ __attribute__((aligned(16))) uint32_t image[IMAGE / 4];
     Block o;
-    if (!kv_block(a, blocks, o) || o.page < 0) return;
-    const int tid = threadIdx.x, l = tid % LANES;
+    if (!kv_block(a, blocks, o)) return;
+    const S sh(o);
+    const uint16_t *src = o.values ? v : k;
+    const int64_t stride = o.values ? v_stride : k_stride;
+    us8 raw[S::ROUNDS][S::CH];
+#pragma unroll
+    for (int i = 0; i < S::ROUNDS; ++i) {
+        const int t = sh.quad(i) * 4 + sh.t4;
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) {
+            raw[i][c] = us8{0, 0, 0, 0, 0, 0, 0, 0};
+            if (t >= o.lo && t < o.hi)
+                raw[i][c] = *reinterpret_cast<const us8 *>(src + (o.row + t) * stride + o.head * D + sh.dim(c));
+        }
+    }
+    if (o.page < 0) return;
     const int page_size = 1 << a.page_shift, in_page = (o.block * 64) & (page_size - 1);
     uint8_t *part = kv_part(a, o.page, o.head);
     const int codes = kv_code_bytes(FMT, page_size, D);
     float *arrays = reinterpret_cast<float *>(part + 2 * codes) + (o.values ? kv_arrays(FMT) / 2 * page_size : 0);
-    const uint16_t *src = o.values ? v : k;
-    const int64_t stride = o.values ? v_stride : k_stride;
 
-    for (int t0 = o.lo; t0 < o.hi; t0 += STEP) {
-        const int t = t0 + tid / LANES;
-        const bool have = t < o.hi;
-        us8 raw = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (have) raw = *reinterpret_cast<const us8 *>(src + (o.row + t) * stride + o.head * D + l * 8);
-        float x[8];
+#pragma unroll
+    for (int i = 0; i < S::ROUNDS; ++i) {
+        const int quad = sh.quad(i), t = quad * 4 + sh.t4;
+        const bool have = t >= o.lo && t < o.hi;
+        if (!__any(have)) break;
+        float x[S::CH][8];
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = to_f32<BF16>(raw[i]);
-            top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-        }
-        top = across<LANES>(top, [](uint32_t p, uint32_t q) { return max(p, q); });
+        for (int c = 0; c < S::CH; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[c][e] = to_f32<BF16>(raw[i][c][e]);
+                top = max(top, __float_as_uint(x[c][e]) & 0x7fffffffu);
+            }
+        top = across<S::LANES>(top, [](uint32_t p, uint32_t q) { return max(p, q); });
         const bool bad = top >= 0x7f800000u;         // an infinity or a NaN
         float scale, low = 0.f;
-        uint32_t code[8];
+        uint32_t w[S::CH][2];                        // 8 bits: codes in bytes; 4 bits: the same before they are packed
         if constexpr (I8) {
             const float amax = __uint_as_float(top), inv = fminf(127.f / amax, FLT_MAX);
             scale = amax / 127.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) code[i] = bad ? 128u : (uint32_t)((int)rintf(x[i] * inv) + 128);
-        } else {
-            float lo = x[0], hi = x[0];
+            for (int c = 0; c < S::CH; ++c)
 #pragma unroll
-            for (int i = 1; i < 8; ++i) {
-                lo = fminf(lo, x[i]);
-                hi = fmaxf(hi, x[i]);
-            }
-            lo = across<LANES>(lo, [](float p, float q) { return fminf(p, q); });
-            hi = across<LANES>(hi, [](float p, float q) { return fmaxf(p, q); });
+                for (int h = 0; h < 2; ++h) {
+                    w[c][h] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[c][h] |= (bad ? 128u : (uint32_t)((int)rintf(x[c][4 * h + e] * inv) + 128)) << (8 * e);
+                }
+        } else {
+            float lo = x[0][0], hi = x[0][0];
+#pragma unroll
+            for (int c = 0; c < S::CH; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    lo = fminf(lo, x[c][e]);
+                    hi = fmaxf(hi, x[c][e]);
+                }
+            lo = across<S::LANES>(lo, [](float p, float q) { return fminf(p, q); });
+            hi = across<S::LANES>(hi, [](float p, float q) { return fmaxf(p, q); });
             const float h = 0.5f * hi - 0.5f * lo, inv = fminf(15.f / h, FLT_MAX);
             scale = h / 7.5f;
             low = bad ? 0.f : lo;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) code[i] = bad ? 0u : (uint32_t)(int)rintf((0.5f * x[i] - 0.5f * lo) * inv);
-        }
-        if (have && l == 0) {
-            const int at = in_page + t;
-            arrays[at] = bad ? __uint_as_float(0x7fc00000u) : scale;
-            if constexpr (!I8) arrays[page_size + at] = low;
-        }
-        if (!o.values) {
-            uint8_t *to = part + key_byte<FMT, D>(in_page + t, l * 8);
-            if constexpr (I8) {
-                const uint2 w = {code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                                 code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24};
-                if (have) *reinterpret_cast<uint2 *>(to) = w;
-            } else {
-                uint32_t w = 0;
+            for (int c = 0; c < S::CH; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w |= code[i] << (4 * w4_slot(i));
-                if (have) *reinterpret_cast<uint32_t *>(to) = w;
+                for (int g = 0; g < 2; ++g) {
+                    w[c][g] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[c][g] |= (bad ? 0u : (uint32_t)(int)rintf((0.5f * x[c][4 * g + e] - 0.5f * lo) * inv)) << (8 * e);
+                }
+        }
+        if (have && sh.l == 0) {
+            arrays[in_page + t] = bad ? __uint_as_float(0x7fc00000u) : scale;
+            if constexpr (!I8) arrays[page_size + in_page + t] = low;
+        }
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) {
+            if (!o.values) {
+                uint8_t *to = part + key_byte<FMT, D>(in_page + t, sh.dim(c));
+                if constexpr (I8) {
+                    if (have) *reinterpret_cast<uint2 *>(to) = uint2{w[c][0], w[c][1]};
+                } else {
+                    uint32_t n = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) n |= (w[c][e / 4] >> (8 * (e % 4)) & 15u) << (4 * w4_slot(e));
+                    if (have) *reinterpret_cast<uint32_t *>(to) = n;
+                }
+                continue;
             }
-        } else if constexpr (I8) {
-            if (have)
+            int b = sh.dim(c);                       // first byte of the lane's 8
+            if constexpr (!I8) {
+                // dims d and d + 16 share a byte: the lane of d takes the other's codes, two lanes on
 #pragma unroll
-                for (int i = 0; i < 8; ++i) image[value_byte(t, l * 8 + i)] = (uint8_t)code[i];
-        } else {
-            // dim d and dim d + 16 share a byte: the lane of d takes the other's codes from two lanes on
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t w = code[i] | (uint32_t)__shfl_xor((int)code[i], 2) << 4;
-                if (have && (l & 2) == 0) image[value_byte(t, l / 4 * 16 + (l & 1) * 8 + i)] = (uint8_t)w;
+                for (int h = 0; h < 2; ++h) w[c][h] |= (uint32_t)__shfl_xor((int)w[c][h], 2) << 4;
+                b = b / 32 * 16 + b % 16;
+            }
+            turn(w[c][0], w[c][1]);
+            if (quad < 16 && (I8 || (sh.l & 2) == 0)) {
+                image[value_word(quad, b + 2 * sh.t4)] = w[c][0];
+                image[value_word(quad, b + 2 * sh.t4 + 1)] = w[c][1];
             }
         }
     }
     if (!o.values) return;
     __syncthreads();
     uint8_t *to = part + codes + kv_code_bytes(FMT, in_page, D);
-    for (int i = tid; i < IMAGE / 16; i += kThreads) {
-        const u4 w = *reinterpret_cast<const u4 *>(image + i * 16);
+    for (int i = threadIdx.x; i < IMAGE / 16; i += kThreads) {
+        const u4 s = *reinterpret_cast<const u4 *>(image + i * 4);
+        const int m = i / 64 & 3;                    // how its dwords are turned: the same for a wave
+        u4 w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = m == 0 ? s[q] : m == 1 ? s[q ^ 1] : m == 2 ? s[q ^ 2] : s[q ^ 3];
         if (o.lo == 0 && o.hi == 64) {
             *reinterpret_cast<u4 *>(to + i * 16) = w;
             continue;
@@ -196,51 +274,85 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, uint16_t *k
                                                            int64_t v_stride, int blocks)
 {
     constexpr bool I8 = FMT == LOWBIT_KV_I8;
-    constexpr int LANES = D / 8, STEP = kThreads / LANES, IMAGE = kv_code_bytes(FMT, 64, D);
-    __shared__ __attribute__((aligned(16))) uint8_t image[IMAGE];
+    typedef Share<D> S;
+    constexpr int IMAGE = kv_code_bytes(FMT, 64, D), PIECES = (IMAGE / 16 + kThreads - 1) / kThreads;
+    __shared__ __attribute__((aligned(16))) uint32_t image[IMAGE / 4];
     Block o;
     if (!kv_block(a, blocks, o)) return;
-    const int tid = threadIdx.x, l = tid % LANES;
+    const S sh(o);
     const int page_size = 1 << a.page_shift, in_page = (o.block * 64) & (page_size - 1);
     uint16_t *dst = o.values ? v : k;
     const int64_t stride = o.values ? v_stride : k_stride;
-    if (o.page < 0) {
-        const us8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int t = o.lo + tid / LANES; t < o.hi; t += STEP)
-            *reinterpret_cast<us8 *>(dst + (o.row + t) * stride + o.head * D + l * 8) = zero;
-        return;
-    }
-    const uint8_t *part = kv_part(a, o.page, o.head);
+    const uint8_t *part = kv_part(a, max(o.page, 0), o.head);
     const int codes = kv_code_bytes(FMT, page_size, D);
     const float *arrays = reinterpret_cast<const float *>(part + 2 * codes) +
                           (o.values ? kv_arrays(FMT) / 2 * page_size : 0);
-    if (o.values) {
-        const uint8_t *from = part + codes + kv_code_bytes(FMT, in_page, D);
-        for (int i = tid; i < IMAGE / 16; i += kThreads)
-            *reinterpret_cast<u4 *>(image + i * 16) = *reinterpret_cast<const u4 *>(from + i * 16);
-        __syncthreads();
-    }
-    for (int t = o.lo + tid / LANES; t < o.hi; t += STEP) {
-        const float scale = arrays[in_page + t], low = I8 ? 0.f : arrays[page_size + in_page + t];
-        us8 out;
-        uint32_t w[2] = {0, 0};
-        if (!o.values) {
-            const uint8_t *from = part + key_byte<FMT, D>(in_page + t, l * 8);
-            w[0] = *reinterpret_cast<const uint32_t *>(from);
-            if constexpr (I8) w[1] = *reinterpret_cast<const uint32_t *>(from + 4);
-        }
+    float scale[S::ROUNDS], low[S::ROUNDS];
+    uint32_t w[S::ROUNDS][S::CH][2];
+    if (o.page >= 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t c;
-            if constexpr (I8)
-                c = o.values ? image[value_byte(t, l * 8 + i)] : (w[i / 4] >> (8 * (i % 4))) & 255;
-            else
-                c = (o.values ? image[value_byte(t, l / 4 * 16 + (l & 1) * 8 + i)] >> (l & 2 ? 4 : 0)
-                              : w[0] >> (4 * w4_slot(i))) & 15;
-            const float value = I8 ? (float)((int)c - 128) * scale : __builtin_fmaf((float)c, scale, low);
-            out[i] = from_f32<BF16>(value);
+        for (int i = 0; i < S::ROUNDS; ++i) {
+            const int t = sh.quad(i) * 4 + sh.t4;
+            if (t < o.lo || t >= o.hi) continue;
+            scale[i] = arrays[in_page + t];
+            if constexpr (!I8) low[i] = arrays[page_size + in_page + t];
+            if (!o.values)
+#pragma unroll
+                for (int c = 0; c < S::CH; ++c) {
+                    const uint32_t *from = reinterpret_cast<const uint32_t *>(part + key_byte<FMT, D>(in_page + t, sh.dim(c)));
+                    w[i][c][0] = from[0];
+                    if constexpr (I8) w[i][c][1] = from[1];
+                }
         }
-        *reinterpret_cast<us8 *>(dst + (o.row + t) * stride + o.head * D + l * 8) = out;
+        if (o.values) {
+            const u4 *from = reinterpret_cast<const u4 *>(part + codes + kv_code_bytes(FMT, in_page, D));
+            u4 s[PIECES];
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                const int i = p * kThreads + threadIdx.x;
+                if (i < IMAGE / 16) s[p] = from[i];
+            }
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                const int i = p * kThreads + threadIdx.x, m = i / 64 & 3;
+                u4 u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) u[q] = m == 0 ? s[p][q] : m == 1 ? s[p][q ^ 1] : m == 2 ? s[p][q ^ 2] : s[p][q ^ 3];
+                if (i < IMAGE / 16) *reinterpret_cast<u4 *>(image + i * 4) = u;
+            }
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < S::ROUNDS; ++i) {
+        const int quad = sh.quad(i), t = quad * 4 + sh.t4;
+        const bool have = t >= o.lo && t < o.hi;
+        if (!__any(have)) break;
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) {
+            us8 out = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (o.page >= 0) {
+                if (o.values) {
+                    const int b = I8 ? sh.dim(c) : sh.dim(c) / 32 * 16 + sh.dim(c) % 16, q = min(quad, 15);
+                    w[i][c][0] = image[value_word(q, b + 2 * sh.t4)];
+                    w[i][c][1] = image[value_word(q, b + 2 * sh.t4 + 1)];
+                    turn_back(w[i][c][0], w[i][c][1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float value;
+                    if constexpr (I8) {
+                        value = (float)((int)(w[i][c][e / 4] >> (8 * (e % 4)) & 255u) - 128) * scale[i];
+                    } else {
+                        const uint32_t n = o.values ? w[i][c][e / 4] >> (8 * (e % 4) + (sh.l & 2 ? 4 : 0))
+                                                    : w[i][c][0] >> (4 * w4_slot(e));
+                        value = __builtin_fmaf((float)(n & 15u), scale[i], low[i]);
+                    }
+                    out[e] = from_f32<BF16>(value);
+                }
+            }
+            if (have) *reinterpret_cast<us8 *>(dst + (o.row + t) * stride + o.head * D + sh.dim(c)) = out;
+        }
     }
 }
 

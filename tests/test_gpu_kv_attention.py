@@ -164,6 +164,10 @@ def test_scales_of_all_sizes(fmt):
         for e in (-100, -20, 0, 40, 100):
             x = torch.from_numpy(np.ldexp(q, e)).to(torch.bfloat16)
             check(cache, batch, 4, "bf16", rng, q=x, scale=float(np.ldexp(0.125, -e)), what="2^%d" % e)
+        # rows that differ by up to 2^30, and by a little
+        for spread in (30, 7):
+            x = torch.from_numpy(q * np.ldexp(1.0, -rng.integers(0, spread + 1, (len(q), 1, 1)))).to(torch.bfloat16)
+            check(cache, batch, 4, "bf16", rng, q=x, scale=8.0, what="spread %d" % spread)
         q = torch.from_numpy(q).to(torch.float16) * 1024
         check(cache, batch, 4, "f16", rng, q=q, scale=0.125 / 1024)
         q = rows(rng, batch.rows, 4, 64, torch.bfloat16)
