@@ -35,6 +35,23 @@ constexpr int kTile = 64;                // tokens of a step: one block of a pag
 constexpr int kMaxItems = 512;           // items that are cut into pieces
 constexpr int kMinPiece = 4;             // blocks that a workgroup takes at least: one for each wave
 
+// n / d and n % d for 0 <= n < 2^31 by one product: m = ceil(2^(31 + b) / d) with 2^(b - 1) < d <= 2^b
+struct Divisor {
+    int d, shift;
+    uint32_t m;
+    __host__ Divisor(int by = 1) : d(by), shift(0), m(0)
+    {
+        int b = 0;
+        while (((int64_t)1 << b) < by) ++b;
+        if (by > 1) {
+            shift = b - 1;
+            m = (uint32_t)((((uint64_t)1 << (31 + b)) + by - 1) / by);
+        }
+    }
+    __device__ __forceinline__ int of(int n) const { return d == 1 ? n : (int)(__umulhi((uint32_t)n, m) >> shift); }
+    __device__ __forceinline__ int rest(int n) const { return n - of(n) * d; }
+};
+
 struct AttnArgs {
     KvArgs kv;
     const uint16_t *q;
@@ -42,9 +59,10 @@ struct AttnArgs {
     int q_heads, group, window;
     float scale2;                        // scale * log2(e)
     uint16_t *y;
+    Divisor by_group, by_tiles, by_heads;
     int tiles;                           // row tiles of a sequence; item = sequence * tiles + tile
     int64_t over, upto;                  // sequences of over < n * group <= upto rows are this launch's
-    int share;                           // 0: a workgroup takes an item's tokens whole; else pieces that they make, items aside
+    int share, fill;                     // 0: a workgroup takes an item's tokens whole; else how many pieces to make of all
     float *part_o;                       // [slots][heads][rows][dim]
     float2 *part_ml;                     // [slots][heads][rows]: maximum and sum of each row's softmax
     int4 *cuts;                          // [0]: how many items are cut; then item, first slot and pieces of each
@@ -65,7 +83,7 @@ __device__ __forceinline__ Span attn_rows(const AttnArgs &a, const KvSeq &s, int
     t.s = s;
     t.r0 = r0;
     t.nr = nr;
-    const int i0 = t.r0 / a.group, i1 = (t.r0 + max(t.nr, 1) - 1) / a.group;
+    const int i0 = a.by_group.of(t.r0), i1 = a.by_group.of(t.r0 + max(t.nr, 1) - 1);
     const int window = a.window > 0 ? min(a.window, max(t.s.len, 1)) : max(t.s.len, 1);
     const int64_t cap = (int64_t)a.kv.width << a.kv.page_shift;
     t.hi = (int)min((int64_t)max(t.s.pos0 + i1 + 1, 0), cap);
@@ -84,10 +102,12 @@ __device__ __forceinline__ Span attn_span(const AttnArgs &a, int b, int tile, in
     return attn_rows(a, s, tile * rows, ours ? (int)min((int64_t)rows, all - tile * rows) : 0);
 }
 
-// The items' tokens cut into pieces of equal size, so that workgroups end together whatever the lengths are: with `share`
-// pieces' worth of blocks in all, an item of n blocks makes ceil(n / size) pieces, at most share + items of them; those of
-// items that are cut, at most 2 * share, have slots for their results.  Nothing is cut where no item is much longer than a
-// piece.  Every wave works this out for itself from the lengths, 64 items at a time.
+// The items' tokens cut into pieces of equal size, so that workgroups end together whatever the lengths are.  An item of n
+// blocks makes ceil(n / size) pieces, so `there` items of T blocks in all make about T / size + there / 2.  Few rows, bound
+// by memory: T / size as many as are resident at once, or twice that where many items leave odd ends.  Tiles, bound by the
+// compute units: pieces to fill these once, or a whole number of times.  Nothing is cut where no item is much longer than a
+// piece.  Those of items that are cut, at most 2 T / size, have slots for their results.  Every wave works this out for
+// itself from the lengths, 64 items at a time, the last tiles of a sequence, its longest, first.
 struct Piece {
     int item, piece;                     // the item, which of its pieces
     int count, size;                     // its pieces, blocks of a piece
@@ -96,40 +116,42 @@ struct Piece {
 };
 __device__ __forceinline__ int item_blocks(const AttnArgs &a, int item, int rows)
 {
-    if (item >= a.kv.count * a.tiles) return -1;
-    const Span t = attn_span(a, item / a.tiles, item % a.tiles, rows);
+    if (item < 0) return -1;
+    const Span t = attn_span(a, a.by_tiles.of(item), a.by_tiles.rest(item), rows);
     return t.nr > 0 ? t.end - t.first : -1;
 }
-// the sum of the lanes below and of the lane's own
-__device__ __forceinline__ int wave_scan(int v)
+// f over the lanes below and the lane's own: within rows of 16, then row by row (0 is the identity)
+template <typename F>
+__device__ __forceinline__ int wave_scan(int v, F f)
 {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        v += lane >= d ? u : 0;
-    }
-    return v;
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+    return f(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
 }
+__device__ __forceinline__ int plus(int p, int q) { return p + q; }
+__device__ __forceinline__ int larger(int p, int q) { return max(p, q); }
+
 // the piece of number `want`; false: there is none
 __device__ __forceinline__ bool find_piece(const AttnArgs &a, int rows, int want, Piece &o)
 {
     constexpr int CHUNKS = kMaxItems / 64;
     const int lane = threadIdx.x & 63, items = a.kv.count * a.tiles;
-    int n[CHUNKS], most = 0;
+    int n[CHUNKS], most = 0, there = 0;
     uint32_t total = 0;                              // in fours: an item has up to 2^24 blocks
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-        n[c] = c * 64 < items ? item_blocks(a, c * 64 + lane, rows) : -1;
+        n[c] = c * 64 < items ? item_blocks(a, items - 1 - c * 64 - lane, rows) : -1;
         total += (uint32_t)(max(n[c], 0) + 3) >> 2;
         most = max(most, n[c]);
+        there += __popcll(__ballot(n[c] >= 0));
     }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        total += __shfl_xor(total, d);
-        most = max(most, __shfl_xor(most, d));
-    }
-    const int even = max((int)((((int64_t)total << 2) + a.share - 1) / a.share), kMinPiece);
+    total = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)total, plus), 63);
+    most = __builtin_amdgcn_readlane(wave_scan(most, larger), 63);
+    const int wanted = a.fill ? (there / 2 / a.share + 1) * a.share - there / 2 : there > a.share / 2 ? 2 * a.share : a.share;
+    const int even = max((int)((((int64_t)total << 2) + wanted - 1) / wanted), kMinPiece);
     o.size = __builtin_amdgcn_readfirstlane(most <= even + even / 2 ? max(most, 1) : even);
     int before = 0, slots = 0;
     o.cuts = 0;
@@ -141,12 +163,12 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, int rows, int want
         if (c * 64 >= items) break;
         const uint64_t cut = __ballot(n[c] > o.size);
         const int mine = n[c] < 0 ? 0 : max((n[c] + o.size - 1) / o.size, 1), kept = mine > 1 ? mine : 0;
-        const int upto = wave_scan(mine), kept_upto = wave_scan(kept);
+        const int upto = wave_scan(mine, plus), kept_upto = wave_scan(kept, plus);
         const int first = before + upto - mine;
         const uint64_t hit = __ballot((first <= want) & (want < first + mine));
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
-            o.item = c * 64 + l;
+            o.item = items - 1 - c * 64 - l;
             o.piece = want - __builtin_amdgcn_readlane(first, l);
             o.count = __builtin_amdgcn_readlane(mine, l);
             o.slot = __builtin_amdgcn_readlane(slots + kept_upto - kept, l);
@@ -175,7 +197,7 @@ __device__ __forceinline__ void put_result(const AttnArgs &a, const Span &t, int
                                            int rr, int d, f4 v, float top, float sum)
 {
     if (pieces == 1) {
-        const int r = t.r0 + rr, i = r / a.group, h = r % a.group;
+        const int r = t.r0 + rr, i = a.by_group.of(r), h = a.by_group.rest(r);
         const ushort4 w = {round_out<BF16>(v[0]), round_out<BF16>(v[1]), round_out<BF16>(v[2]), round_out<BF16>(v[3])};
         *reinterpret_cast<ushort4 *>(a.y + ((int64_t)(t.s.row0 + i) * a.q_heads + kvh * a.group + h) * D + d) = w;
     } else {
@@ -354,6 +376,9 @@ struct Rows {
     typedef typename S::Acc Acc;
     static constexpr bool I8 = FMT == LOWBIT_KV_I8;
     static constexpr int KS = D / S::STEP, M = D / COLS, EL = S::EL, QN = S::QN, PU = 64 / S::STEP;
+    // fp16 results take their weights in two fp16 parts, p = rne(p) + rne(p - rne(p)): one alone costs a result of fp16 as
+    // much as its own rounding (4 bits: twice, as codes and minima are summed apart); to one of bf16 it adds 2 %
+    static constexpr int PARTS = BF16 ? 1 : 2;
     typedef Codes<FMT, D> C;
     h8 qf[NQ][KS];
     float c[NQ], qsum[NQ];               // the row's factor of the scales; the sum of its operands
@@ -400,7 +425,7 @@ struct Rows {
         clear();
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
-            const int r = r0 + (x * COLS + n < nr ? x * COLS + n : 0), i = r / a.group, h = r % a.group;
+            const int r = r0 + (x * COLS + n < nr ? x * COLS + n : 0), i = a.by_group.of(r), h = a.by_group.rest(r);
             const uint16_t *src = a.q + (int64_t)(seq.row0 + i) * a.q_stride + (kvh * a.group + h) * D;
             see_hi[x] = seq.pos0 + i + 1;
             see_lo[x] = a.window > 0 ? see_hi[x] - min(a.window, max(seq.len, 1)) : 0;
@@ -481,7 +506,7 @@ struct Rows {
     // masked: some row does not see all of the block, whose first token is t0, or its page is missing.
     template <typename KS_, typename KL, typename VS, typename VL>
     __device__ __forceinline__ void weigh(Acc (&acc)[NQ][S::TILES], KS_ ks, KL kl, VS vs, VL vl, bool masked, bool paged,
-                                          int64_t t0, int j, h8 (&pf)[NQ][PU])
+                                          int64_t t0, int j, h8 (&pf)[PARTS][NQ][PU])
     {
         constexpr int T = 64 / QN;       // tokens from one q to the next
         auto s = [&](int x, int q, int e) -> float { return acc[x][q * 4 / EL][q * 4 % EL + e]; };
@@ -596,25 +621,32 @@ struct Rows {
 #pragma unroll
             for (int u = 0; u < PU; ++u)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) pf[x][u][e] = (_Float16)s(x, 2 * u + e / 4, C::order(e % 4));
+                for (int e = 0; e < 8; ++e) {
+                    const float p = s(x, 2 * u + e / 4, C::order(e % 4));
+                    pf[0][x][u][e] = (_Float16)p;
+                    if constexpr (PARTS == 2) pf[1][x][u][e] = (_Float16)(p - (float)pf[0][x][u][e]);
+                }
     }
 };
 
 // Few rows: a workgroup of W waves has the 16 * NQ rows of an item, and each wave every W-th block of tokens of its
 // piece.  A block's loads are under way while the one before is worked on: its keys are asked for as soon as the last
 // product with the keys before them has begun, scales and values likewise, so that they need no registers of their own.
-template <int FMT, int D, bool BF16, int NQ, int W>
-__global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_kernel(AttnArgs a)
+template <int FMT, int D, bool BF16, int NQ>
+__global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel(AttnArgs a)
 {
     constexpr bool I8 = FMT == LOWBIT_KV_I8;
-    constexpr int ROWS = 16 * NQ, KS = D / 32, M = D / 16, DH = D < 128 ? D : 128, LD = DH + 4;
+    constexpr int W = 4, ROWS = 16 * NQ, KS = D / 32, M = D / 16, DH = D < 128 ? D : 128, LD = DH + 4;
+    constexpr int PARTS = Rows<FMT, D, BF16, 16, NQ, false>::PARTS;
     typedef Codes<FMT, D> C;
     __shared__ __attribute__((aligned(16))) float o_s[W * 16 * LD];
-    __shared__ float m_s[W][16], l_s[W][16], b_s[W][16];
+    __shared__ float m_s[NQ][W][16], l_s[NQ][W][16], b_s[NQ][W][16];
     __shared__ int e_s[W];
+    __shared__ float g_s[NQ][W][16], add_s[NQ][16], top_s[NQ][16], sum_s[NQ][16];
 
-    const int kvh = blockIdx.x % a.kv.heads, number = blockIdx.x / a.kv.heads;
-    Piece pc = {a.share > 0 ? 0 : a.kv.count * a.tiles - 1 - number, 0, 1, 0, 0, 0, 0};   // whole items: the last tiles, the longest, first
+    const int kvh = a.by_heads.rest(blockIdx.x), number = a.by_heads.of(blockIdx.x);
+    // whole items: the last tiles of a sequence, its longest, first
+    Piece pc = {a.share > 0 ? 0 : a.kv.count * a.tiles - 1 - number, 0, 1, 0, 0, 0, 0};
     if (a.share > 0) {
         const bool found = find_piece(a, ROWS, number, pc);
         if (number == 0 && kvh == 0 && threadIdx.x == 0) a.cuts[0] = int4{pc.cuts, 0, 0, 0};
@@ -622,8 +654,8 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
         if (pc.count > 1 && pc.piece == 0 && kvh == 0 && threadIdx.x == 0)
             a.cuts[1 + pc.cut] = int4{pc.item, pc.slot, pc.count, 0};
     }
-    const int item = __builtin_amdgcn_readfirstlane(pc.item), b = item / a.tiles;
-    const Span t = attn_span(a, b, item % a.tiles, ROWS);
+    const int item = __builtin_amdgcn_readfirstlane(pc.item), b = a.by_tiles.of(item);
+    const Span t = attn_span(a, b, a.by_tiles.rest(item), ROWS);
     if (t.nr <= 0) return;
     const int begin = __builtin_amdgcn_readfirstlane(t.first + pc.piece * pc.size);
     const int end = __builtin_amdgcn_readfirstlane(pc.count > 1 ? min(begin + pc.size, t.end) : t.end);
@@ -708,7 +740,7 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
         const float norm = ldexpf(1.f, kTop - w.E);
 #pragma unroll
         for (int q = 0; q < 4; ++q) r.vs[q] *= norm;
-        h8 pf[NQ][2];
+        h8 pf[PARTS][NQ][2];
         auto of = [](const f4 *v) { return [v](int q) { return v[q]; }; };
         w.weigh(s, of(r.ks), of(r.kl), of(r.vs), of(r.vl), masked, page >= 0, t0, j, pf);
         __builtin_amdgcn_sched_barrier(0);
@@ -721,7 +753,9 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
                 const h8 vf = C::value(r.vr, i, u, mant);
 #pragma unroll
                 for (int x = 0; x < NQ; ++x)
-                    w.o[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[x][u], w.o[x][i], 0, 0, 0);
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        w.o[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[part][x][u], w.o[x][i], 0, 0, 0);
             }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MORE) r.load_values(part, next_at, lane, page_size);
@@ -745,49 +779,63 @@ __global__ __launch_bounds__(W * 64, D * NQ > 128 ? 1 : 2) void kv_attention_ker
         step(std::false_type{}, part_of(page), 0);
     }
 
-    // the waves' results joined, 16 rows and up to 128 dims at a time
+    // the waves' results joined: what each counts for in a row, then 16 rows and up to 128 dims at a time
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
         w.l[x] = column_sum(w.l[x]);
         w.bias[x] = column_sum(w.bias[x]);
+        if (j == 0) {
+            m_s[x][wave][n] = w.mc[x];
+            l_s[x][wave][n] = w.l[x];
+            b_s[x][wave][n] = w.bias[x];
+        }
+    }
+    if (lane == 0) e_s[wave] = w.E - kTop;
+    __syncthreads();
+    if (threadIdx.x < ROWS) {
+        const int x = threadIdx.x / 16, row = threadIdx.x % 16;
+        float top = -INFINITY, sum = 0.f, add = 0.f, f[W];
+#pragma unroll
+        for (int q = 0; q < W; ++q) top = l_s[x][q][row] == 0.f ? top : fmaxf(top, m_s[x][q][row]);
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+            f[q] = l_s[x][q][row] == 0.f ? 0.f : exp2_fast(m_s[x][q][row] - top);
+            sum += f[q] * l_s[x][q][row];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+            add += f[q] == 0.f ? 0.f : b_s[x][q][row] * (f[q] * inv);
+            g_s[x][q][row] = ldexpf(f[q] * inv, e_s[q]);
+        }
+        add_s[x][row] = add;
+        top_s[x][row] = top;
+        sum_s[x][row] = sum;
+    }
+#pragma unroll
+    for (int x = 0; x < NQ; ++x)
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += DH) {
             if (x > 0 || d0 > 0) __syncthreads();
-            if (j == 0) {
-                m_s[wave][n] = w.mc[x];
-                l_s[wave][n] = w.l[x];
-                b_s[wave][n] = w.bias[x];
-                if (n == 0) e_s[wave] = w.E - kTop;
-            }
 #pragma unroll
             for (int i = 0; i < DH / 16; ++i)
                 *reinterpret_cast<f4 *>(o_s + (wave * 16 + n) * LD + 16 * i + 4 * j) = w.o[x][d0 / 16 + i];
             __syncthreads();
-            for (int at = threadIdx.x; at < 16 * DH / 4; at += W * 64) {
-                const int row = at / (DH / 4), d = at % (DH / 4) * 4, rr = x * 16 + row;
-                if (rr >= t.nr) continue;
-                float top = -INFINITY, sum = 0.f, f[W];
-#pragma unroll
-                for (int q = 0; q < W; ++q) top = l_s[q][row] == 0.f ? top : fmaxf(top, m_s[q][row]);
+            for (int at = threadIdx.x; at < min(t.nr - 16 * x, 16) * (DH / 4); at += W * 64) {
+                const int row = at / (DH / 4), d = at % (DH / 4) * 4;
+                const float add = add_s[x][row];
+                f4 v = {add, add, add, add};
 #pragma unroll
                 for (int q = 0; q < W; ++q) {
-                    f[q] = l_s[q][row] == 0.f ? 0.f : exp2_fast(m_s[q][row] - top);
-                    sum += f[q] * l_s[q][row];
-                }
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                f4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int q = 0; q < W; ++q) {
-                    if (l_s[q][row] == 0.f) continue;
+                    const float g = g_s[x][q][row];
                     const f4 ow = *reinterpret_cast<const f4 *>(o_s + (q * 16 + row) * LD + d);
-                    const float g = f[q] * inv;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += ldexpf(ow[e] * g, e_s[q]) + b_s[q][row] * g;
+                    for (int e = 0; e < 4; ++e) v[e] = g == 0.f ? v[e] : __builtin_fmaf(ow[e], g, v[e]);
                 }
-                put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, rr, d0 + d, v, top, sum);
+                put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, 16 * x + row, d0 + d, v, top_s[x][row],
+                                    sum_s[x][row]);
             }
         }
-    }
 }
 
 // Many rows: a workgroup of eight waves has 16 * NQ rows of an item in each, and takes the blocks of its piece one by one.
@@ -816,8 +864,9 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
     h8 *kfrag = reinterpret_cast<h8 *>(lds), *vfrag = kfrag + 2 * FRAGS * 64;   // [2][FRAGS][64] each
     float *arrays = reinterpret_cast<float *>(vfrag + 2 * FRAGS * 64);          // [4][K, V][scale, minimum][64]
 
-    const int kvh = blockIdx.x % a.kv.heads, number = blockIdx.x / a.kv.heads;
-    Piece pc = {a.share > 0 ? 0 : a.kv.count * a.tiles - 1 - number, 0, 1, 0, 0, 0, 0};   // whole items: the last tiles, the longest, first
+    const int kvh = a.by_heads.rest(blockIdx.x), number = a.by_heads.of(blockIdx.x);
+    // whole items: the last tiles of a sequence, its longest, first
+    Piece pc = {a.share > 0 ? 0 : a.kv.count * a.tiles - 1 - number, 0, 1, 0, 0, 0, 0};
     if (a.share > 0) {
         const bool found = find_piece(a, ROWS, number, pc);
         if (number == 0 && kvh == 0 && threadIdx.x == 0) a.cuts[0] = int4{pc.cuts, 0, 0, 0};
@@ -825,8 +874,8 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
         if (pc.count > 1 && pc.piece == 0 && kvh == 0 && threadIdx.x == 0)
             a.cuts[1 + pc.cut] = int4{pc.item, pc.slot, pc.count, 0};
     }
-    const int item = __builtin_amdgcn_readfirstlane(pc.item), b = item / a.tiles;
-    const Span t = attn_span(a, b, item % a.tiles, ROWS);
+    const int item = __builtin_amdgcn_readfirstlane(pc.item), b = a.by_tiles.of(item);
+    const Span t = attn_span(a, b, a.by_tiles.rest(item), ROWS);
     if (t.nr <= 0) return;
     const int begin = __builtin_amdgcn_readfirstlane(t.first + pc.piece * pc.size);
     const int end = __builtin_amdgcn_readfirstlane(pc.count > 1 ? min(begin + pc.size, t.end) : t.end);
@@ -954,10 +1003,12 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
 
     const int count = end - begin;
     typename R::Acc s[1][Sh::TILES];
-    h8 pf[1][PU];
+    h8 pf[R::PARTS][1][PU];
     auto no_weights = [&] {
 #pragma unroll
-        for (int u = 0; u < PU; ++u) pf[0][u] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+        for (int part = 0; part < R::PARTS; ++part)
+#pragma unroll
+            for (int u = 0; u < PU; ++u) pf[part][0][u] = h8{0, 0, 0, 0, 0, 0, 0, 0};
     };
     no_weights();
     // Products of the values of block i - 1, then of the keys of block i; kAhead operands are under way from LDS, and the
@@ -974,7 +1025,8 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
 #pragma unroll
         for (int q = 0; q < FRAGS; ++q) {
             const h8 f = ring[q % kAhead];
-            w.o[0][q / PU] = Sh::mul(f, pf[0][q % PU], w.o[0][q / PU]);
+#pragma unroll
+            for (int part = 0; part < R::PARTS; ++part) w.o[0][q / PU] = Sh::mul(f, pf[part][0][q % PU], w.o[0][q / PU]);
             if (q + kAhead < ALL) ask(q + kAhead);
             if (KEYS)
 #pragma unroll
@@ -1049,57 +1101,102 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
         }
 }
 
-// The pieces of a cut item's rows joined: each has its own normalised result, and weighs sum * 2^maximum.  A workgroup takes
-// `per` rows of one head one by one, dim / 4 lanes for each of the row's pieces, 256 / (dim / 4) pieces at a time.
-template <int D, bool BF16>
-__global__ __launch_bounds__(256) void kv_attention_join_kernel(AttnArgs a, int rows, int per, int groups)
+// The pieces of a cut item's rows joined: each has its own normalised result, and weighs sum * 2^maximum.  The items of both
+// launches are joined by one, whose workgroups take `per` rows of an item and head at a time, dim / 4 lanes a row.  Where an
+// item has few pieces each row is the work of its own lanes; else rows come one by one, 256 / (dim / 4) pieces at a time.
+struct JoinArgs {
+    AttnArgs a[2];                       // share = 0: nothing of it is cut
+    int rows[2], per[2], groups[2], cuts[2];
+    int grid[2];                         // workgroups of each
+};
+constexpr int kJoinGroups = 2048;        // as many workgroups as are resident at once
+constexpr int kFewPieces = 8;
+
+template <int D, bool BF16, bool TILES>
+__global__ __launch_bounds__(256, 6) void kv_attention_join_kernel(JoinArgs p)
 {
     constexpr int LANES = D / 4, G = 256 / LANES;
     __shared__ f4 part[G][LANES];
     __shared__ float sums[G];
-    const int kvh = blockIdx.x % a.kv.heads, r0 = blockIdx.x / a.kv.heads % groups * per;
-    const int cut = blockIdx.x / a.kv.heads / groups;
-    const int4 it = a.cuts[1 + cut];
-    if (cut >= a.cuts[0].x) return;
-    const Span t = attn_span(a, it.x / a.tiles, it.x % a.tiles, rows);
-    const int64_t step = (int64_t)a.kv.heads * rows;
+    const int which = TILES && (int)blockIdx.x >= p.grid[0];
+    const AttnArgs &a = p.a[which];
+    const int heads = a.kv.heads, rows = p.rows[which], per = p.per[which], groups = p.groups[which], grid = p.grid[which];
     const int lane = threadIdx.x & 63, g = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
-    for (int rr = r0; rr < min(r0 + per, t.nr); ++rr) {
-        const int64_t first = ((int64_t)it.y * a.kv.heads + kvh) * rows + rr;
-        float top = -INFINITY;
-        for (int i = lane; i < it.z; i += 64) {
-            const float2 ml = a.part_ml[first + i * step];
-            if (ml.y != 0.f) top = fmaxf(top, ml.x);
-        }
+    for (int at = blockIdx.x - (which ? p.grid[0] : 0);; at += grid) {
+        const int cut = at / heads / groups;
+        if (cut >= p.cuts[which]) return;
+        const int4 it = a.cuts[1 + cut];             // asked for beside their number
+        if (cut >= a.cuts[0].x) return;
+        const int kvh = at % heads, r0 = at / heads % groups * per;
+        const int item = __builtin_amdgcn_readfirstlane(it.x), pieces = __builtin_amdgcn_readfirstlane(it.z);
+        const Span t = attn_span(a, a.by_tiles.of(item), a.by_tiles.rest(item), rows);
+        const int64_t step = (int64_t)heads * rows, base = ((int64_t)it.y * heads + kvh) * rows;
+        if (TILES && per > 1 && pieces <= kFewPieces) {
+            const int rr = r0 + g;
+            if (g >= per || rr >= t.nr) continue;
+            float2 ml[kFewPieces];
+            f4 v = {0.f, 0.f, 0.f, 0.f};
+            float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-        f4 v = {0.f, 0.f, 0.f, 0.f};
-        float sum = 0.f;
+            for (int i = 0; i < kFewPieces; ++i) {
+                ml[i] = a.part_ml[base + rr + min(i, pieces - 1) * step];
+                if (i >= pieces) ml[i].y = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kFewPieces; ++i) top = ml[i].y != 0.f ? fmaxf(top, ml[i].x) : top;
+#pragma unroll
+            for (int i0 = 0; i0 < kFewPieces; i0 += 4) {
+                if (i0 >= pieces) break;
+                f4 o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = *reinterpret_cast<const f4 *>(a.part_o + (base + rr + min(i0 + i, pieces - 1) * step) * D + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = ml[i0 + i].y == 0.f ? 0.f : ml[i0 + i].y * exp2_fast(ml[i0 + i].x - top);
+                    sum += f;
+                    v += i0 + i < pieces ? o[i] * f : f4{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+            put_result<D, BF16>(a, t, 1, 0, kvh, rows, rr, d, v * (sum == 0.f ? 0.f : 1.f / sum), 0.f, 0.f);
+            continue;
+        }
+        for (int rr = r0; rr < min(r0 + per, t.nr); ++rr) {
+            float top = -INFINITY;
+            for (int i = lane; i < pieces; i += 64) {
+                const float2 ml = a.part_ml[base + rr + i * step];
+                if (ml.y != 0.f) top = fmaxf(top, ml.x);
+            }
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+            f4 v = {0.f, 0.f, 0.f, 0.f};
+            float sum = 0.f;
 #pragma unroll 4
-        for (int i = g; i < it.z; i += G) {
-            const float2 ml = a.part_ml[first + i * step];
-            const f4 o = *reinterpret_cast<const f4 *>(a.part_o + (first + i * step) * D + d);
-            const float f = ml.y == 0.f ? 0.f : ml.y * exp2_fast(ml.x - top);
-            sum += f;
-            v += o * f;
+            for (int i = g; i < pieces; i += G) {
+                const float2 ml = a.part_ml[base + rr + i * step];
+                const f4 o = *reinterpret_cast<const f4 *>(a.part_o + (base + rr + i * step) * D + d);
+                const float f = ml.y == 0.f ? 0.f : ml.y * exp2_fast(ml.x - top);
+                sum += f;
+                v += o * f;
+            }
+            part[g][threadIdx.x % LANES] = v;
+            if (d == 0) sums[g] = sum;
+            __syncthreads();
+            if (threadIdx.x < LANES) {
+                v = f4{0.f, 0.f, 0.f, 0.f};
+                sum = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < G; ++i) {
+                    v += part[i][threadIdx.x];
+                    sum += sums[i];
+                }
+                put_result<D, BF16>(a, t, 1, 0, kvh, rows, rr, d, v * (sum == 0.f ? 0.f : 1.f / sum), 0.f, 0.f);
+            }
+            __syncthreads();                 // the row is read before the next is written
         }
-        if (rr > r0) __syncthreads();                 // the row before is read
-        part[g][threadIdx.x % LANES] = v;
-        if (d == 0) sums[g] = sum;
-        __syncthreads();
-        if (threadIdx.x >= LANES) continue;
-        v = f4{0.f, 0.f, 0.f, 0.f};
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            v += part[i][threadIdx.x];
-            sum += sums[i];
-        }
-        put_result<D, BF16>(a, t, 1, 0, kvh, rows, rr, d, v * (sum == 0.f ? 0.f : 1.f / sum), 0.f, 0.f);
     }
 }
 
-constexpr int kWaves = 4;                // of a workgroup with few rows
 constexpr int kTileRows = 128;
 constexpr int kWholeBlocks = 16;         // blocks up to which an item is not worth a second launch
 constexpr int64_t kFewBeside = 16;       // rows of a sequence up to which it goes with the few, where others have many
@@ -1107,14 +1204,15 @@ constexpr int64_t kFewBeside = 16;       // rows of a sequence up to which it go
 // A launch over the sequences of over < rows * group <= upto
 struct AttnPlan {
     bool tile;
-    int nq, rows;                        // rows of an item: 16 * nq for all waves (few), kTileRows (tile)
+    int nq, rows;                 // rows of an item: 16 * nq for all waves (few), kTileRows (tile)
     int64_t over, upto, pieces, slots;   // workgroups for each head at most, results of pieces
     int tiles, share, cuts;              // cuts: items that are cut, at most
 };
 int64_t plan_bytes(const AttnPlan &p, const KvArgs &a)
 {
     if (p.share == 0) return 0;
-    return p.slots * a.heads * p.rows * (a.dim * 4 + 8) + ((int64_t)p.cuts + 1) * (int64_t)sizeof(int4);
+    // 2 * share cut items have a place also where offsets that go back make more items than there are rows for
+    return p.slots * a.heads * p.rows * (a.dim * 4 + 8) + (2 * (int64_t)p.share + 1) * (int64_t)sizeof(int4);   // whole 16 bytes
 }
 void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int resident)
 {
@@ -1124,9 +1222,11 @@ void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int re
     p.share = cut ? std::max(resident / a.heads, 1) : 0;
     // tiles that there can be: whole ones of all rows, and a sequence's last
     const int64_t there = std::min(items, (int64_t)a.rows * group / p.rows + std::min(a.count, a.rows));
-    p.pieces = cut ? there + p.share : items;
-    p.slots = 2 * p.share;                                   // a cut item has two pieces or more
-    p.cuts = (int)std::min<int64_t>(there, p.share);
+    // T / size is at most 2 * share; a cut item has two pieces or more
+    const int64_t most = 2 * p.share;
+    p.pieces = cut ? there + most : items;
+    p.slots = 2 * most;
+    p.cuts = (int)std::min<int64_t>(there, most);
 }
 // one launch or two: sequences of many rows first
 int attn_plan(const KvArgs &a, int q_heads, AttnPlan *p)
@@ -1151,7 +1251,7 @@ int attn_plan(const KvArgs &a, int q_heads, AttnPlan *p)
     f.rows = 16 * f.nq;
     f.over = 0;
     f.upto = rows > few ? kFewBeside : INT64_MAX;
-    cut_plan(f, a, group, most, a.dim * f.nq > 128 ? 256 : 512 * 4 / kWaves);
+    cut_plan(f, a, group, most, a.dim * f.nq > 128 ? 256 : 512);
     return n;
 }
 
@@ -1174,9 +1274,9 @@ size_t kv_attention_workspace(const KvArgs &a, int q_heads)
 {
     AttnPlan p[2];
     const int n = attn_plan(a, q_heads, p);
-    int64_t most = 0;
-    for (int i = 0; i < n; ++i) most = std::max(most, plan_bytes(p[i], a));
-    return (size_t)most;
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) all += plan_bytes(p[i], a);
+    return (size_t)all;
 }
 
 hipError_t launch_kv_attention(const KvArgs &kv, const void *q, int64_t q_stride, int q_heads, int bf16, float scale,
@@ -1184,15 +1284,19 @@ hipError_t launch_kv_attention(const KvArgs &kv, const void *q, int64_t q_stride
 {
     AttnPlan plans[2];
     const int n = attn_plan(kv, q_heads, plans);
+    JoinArgs joined{};
+    uint8_t *free = static_cast<uint8_t *>(ws);
     auto launch = [&](const AttnPlan &p, auto fmt, auto dim, auto bf) {
         constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
         constexpr bool B = decltype(bf)::value;
         AttnArgs a{kv, static_cast<const uint16_t *>(q), q_stride, q_heads, q_heads / kv.heads, window, scale * kLog2e,
-                   static_cast<uint16_t *>(y), p.tiles, p.over, p.upto, p.share, nullptr, nullptr, nullptr};
+                   static_cast<uint16_t *>(y), Divisor(q_heads / kv.heads), Divisor(p.tiles), Divisor(kv.heads), p.tiles,
+                   p.over, p.upto, p.share, p.tile, nullptr, nullptr, nullptr};
         if (p.share > 0) {
-            a.part_o = static_cast<float *>(ws);
+            a.part_o = reinterpret_cast<float *>(free);
             a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.slots * kv.heads * p.rows * kv.dim);
             a.cuts = reinterpret_cast<int4 *>(a.part_ml + p.slots * kv.heads * p.rows);
+            free += plan_bytes(p, kv);
         }
         const unsigned grid = (unsigned)(p.pieces * kv.heads);
         auto tile = [&](auto cols, auto waves) {
@@ -1216,21 +1320,31 @@ hipError_t launch_kv_attention(const KvArgs &kv, const void *q, int64_t q_stride
             typedef std::integral_constant<int, 32> c32;
             typedef std::integral_constant<int, 4> w4;
             typedef std::integral_constant<int, 8> w8;
-            if constexpr (D == 256) e = tile(c16{}, w8{});
+            if constexpr (D == 256) {
+                e = tile(c16{}, w8{});
+            }
             else e = tile(c32{}, w4{});
         } else {
             auto few = [&](auto nq) {
-                kv_attention_kernel<F, D, B, decltype(nq)::value, kWaves><<<grid, kWaves * 64, 0, s>>>(a);
+                constexpr int NQ = decltype(nq)::value;
+                kv_attention_kernel<F, D, B, NQ><<<grid, 256, 0, s>>>(a);
                 return hipGetLastError();
             };
             if constexpr (D == 64) e = p.nq == 1 ? few(one{}) : p.nq == 2 ? few(two{}) : few(four{});
             else if constexpr (D == 128) e = p.nq == 1 ? few(one{}) : few(two{});
             else e = few(one{});
         }
-        if (e != hipSuccess || p.share == 0) return e;
-        const int per = p.tile ? 4 : 1, most = (int)std::min<int64_t>(p.rows, (int64_t)kv.max_rows * a.group);
-        const int groups = (most + per - 1) / per;
-        kv_attention_join_kernel<D, B><<<(unsigned)((int64_t)p.cuts * kv.heads * groups), 256, 0, s>>>(a, p.rows, per, groups);
+        const int k = &p == plans ? 0 : 1, most = (int)std::min<int64_t>(p.rows, (int64_t)kv.max_rows * a.group);
+        joined.a[k] = a;
+        joined.rows[k] = p.rows;
+        joined.per[k] = p.tile ? 4 : 1;
+        joined.groups[k] = (most + joined.per[k] - 1) / joined.per[k];
+        joined.cuts[k] = p.cuts;
+        if (p.share > 0) joined.grid[k] = (int)std::min<int64_t>((int64_t)p.cuts * kv.heads * joined.groups[k], kJoinGroups);
+        const int grid_all = joined.grid[0] + joined.grid[1];
+        if (e != hipSuccess || k + 1 < n || grid_all == 0) return e;
+        if (plans[0].tile) kv_attention_join_kernel<D, B, true><<<grid_all, 256, 0, s>>>(joined);
+        else kv_attention_join_kernel<D, B, false><<<grid_all, 256, 0, s>>>(joined);
         return hipGetLastError();
     };
     auto with_bf = [&](const AttnPlan &p, auto fmt, auto dim) {

@@ -169,8 +169,8 @@ def attention64(cache, batch, q, scale, window, dtype):
 
     Steps, relative to sums of magnitudes: the score's D products and their scale (D + 6 roundings of binary32, each
     dim at most |q| (|code scale| + |minimum|)); the exponent's two roundings of |score|; p and its sum (a few roundings
-    each, the sum over at most n tokens); p * vscale to fp16 (half a step 2^-11, or half the spacing 2^-25 of what is
-    near zero, in units of 2^(E - 6), E the exponent of the largest value scale that some row of the call sees); the
+    each, the sum over at most n tokens); p * vscale to fp16 (half a step 2^-11 for results of bf16; for those of fp16 the
+    rest in a second part, and half a step of that: 2^-22; or half the spacing 2^-25 of what is near zero, in units of 2^(E - 6), E the exponent of the largest value scale that some row of the call sees); the
     sum over tokens (n roundings); the joining of parts (a few roundings, one exp2 each, of 2^-22); the result's own."""
     rows, Hq, D = q.shape
     y, bound = np.zeros((batch.rows, Hq, D)), np.zeros((batch.rows, Hq, D))
@@ -202,7 +202,7 @@ def attention64(cache, batch, q, scale, window, dtype):
                 size = p @ (np.abs(vc[seen]) + np.abs(vl[seen]))
                 ds = ((D + 8) * U32 * mag + 4 * U32 * np.abs(s)).max(1, keepdims=True)
                 m = len(seen)
-                rel = 2.0 ** -11 + 2 * np.expm1(ds) + (2 * m + 64) * U32 + 2.0 ** -20
+                rel = (2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22) + 2 * np.expm1(ds) + (2 * m + 64) * U32 + 2.0 ** -20
                 fine = vscale[have][np.isfinite(vscale[have])]
                 tiny = m * 2.0 ** -25 * 2.0 ** -6 * (fine.max() if len(fine) else 0) * 128
                 e = size * rel + tiny
