@@ -3,21 +3,31 @@
 //   y[r][h] = sum_j p_j v_j,  p = softmax_j(scale * q[r][h] . k_j)  over the tokens j that row r sees
 //
 // The query heads that share a key/value head and the tokens of a sequence are
-// the rows of one matrix product (row = token * group + head of the group), 16
-// at a time.  Both products run on v_mfma_f32_16x16x32_f16 with the cache as the
-// A operand, straight from memory: the pages hold keys and values in the order of
-// that operand, codes become fp16 exactly in registers (1024 + code is an fp16
-// bit pattern; the bias is then subtracted).  S^T = K Q^T leaves a lane with 4
-// tokens of each 16 for one query, which is the B operand of O^T = V^T P^T with
-// the tokens of a 32 in the order 4j..4j+3, 16+4j..16+4j+3: the probabilities
-// never leave their registers.
+// the rows of one matrix product (row = token * group + head of the group).
+// Both products run on the fp16 matrix instructions with the cache as the A
+// operand: the pages hold keys and values in the order of that operand, and
+// codes become fp16 exactly in registers (1024 + code is an fp16 bit pattern;
+// the bias, and the code's own middle, are then subtracted).  S^T = K Q^T leaves
+// a lane with 4 tokens of each 16 (32x32x16: of each 8) for one query, which is
+// the B operand of O^T = V^T P^T with the tokens of a 32 in the order 4j..4j+3,
+// 16+4j..16+4j+3: the weights never leave their registers.
 //
 // Scales stand outside of the sums over dims (keys) and inside of those over
 // tokens (values): s = kscale * acc (+ kmin * sum of q, 4 bits), and the fp16
-// operand is p * vscale * 2^(14 - E), E the largest exponent of a value scale so
-// far: p <= 1 keeps it under 2^15, and terms down to 2^-28 of the largest keep
-// their 11 bits.  The minima of values enter as sum p * vmin, one number per row.
-// The softmax runs in one pass with a running maximum.
+// operand is p * vscale * 2^(kTop - E), E the largest exponent of a value scale
+// so far.  The minima of values enter as sum p * vmin, one number per row.  The
+// softmax runs in one pass; the maximum that a row's terms are taken to moves
+// only where one passes it by 2^kSlack, so that most blocks rescale nothing.
+// The operand stays under 2^(kSlack + kTop + 1) = 2^15, and terms down to 2^-20 of
+// one at that maximum and scale keep all their 11 bits (fp16's least normal
+// number is 2^-14).
+//
+// Two kernels share this.  Few rows (kv_attention_kernel) read the cache once,
+// and its bytes are the bound: 562 MB of 8 bit cache for 32 tokens of 2 .. 8192
+// tokens each in 107 us, 5.2 TB/s, as fast as a large copy.  Many rows
+// (kv_attention_tile_kernel) are bound by the instructions of a compute unit,
+// matrix and vector ones: 515 GFLOP of a causal prompt in 0.61 ms, 845 TFLOP/s,
+// 70 % of a large library product's rate.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -263,8 +273,9 @@ struct Codes {
     {
         const uint32_t w0 = w[step * 2], w1 = w[step * 2 + 1];
         if constexpr (I8) return from_bytes(w0, w1, (_Float16)1152);
-        return high == 0 ? join(nibble_low(w0, mant), nibble_low(w0 >> 8, mant), nibble_low(w1, mant), nibble_low(w1 >> 8, mant))
-                         : join(nibble_high(w0, mant), nibble_high(w0 >> 8, mant), nibble_high(w1, mant), nibble_high(w1 >> 8, mant));
+        if (high)
+            return join(nibble_high(w0, mant), nibble_high(w0 >> 8, mant), nibble_high(w1, mant), nibble_high(w1 >> 8, mant));
+        return join(nibble_low(w0, mant), nibble_low(w0 >> 8, mant), nibble_low(w1, mant), nibble_low(w1 >> 8, mant));
     }
     static __device__ __forceinline__ h8 value(const u4 *raw, int m, int step, uint32_t mant)
     {
@@ -350,7 +361,10 @@ template <>
 struct Shape<16> {
     typedef f4 Acc;
     static constexpr int QN = 4, STEP = 32, TILES = 4, EL = 4;      // STEP: dims (tokens) that an instruction sums over
-    static __device__ __forceinline__ f4 mul(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ f4 mul(h8 a, h8 b, f4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
     static __device__ __forceinline__ float max_of(float v) { return column_max(v); }
     static __device__ __forceinline__ float sum_of(float v) { return column_sum(v); }
 };
@@ -358,7 +372,10 @@ template <>
 struct Shape<32> {
     typedef float Acc __attribute__((ext_vector_type(16)));
     static constexpr int QN = 8, STEP = 16, TILES = 2, EL = 16;
-    static __device__ __forceinline__ Acc mul(h8 a, h8 b, Acc c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ Acc mul(h8 a, h8 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
     static __device__ __forceinline__ float max_of(float v)
     {
         const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -377,7 +394,8 @@ struct Rows {
     static constexpr bool I8 = FMT == LOWBIT_KV_I8;
     static constexpr int KS = D / S::STEP, M = D / COLS, EL = S::EL, QN = S::QN, PU = 64 / S::STEP;
     // fp16 results take their weights in two fp16 parts, p = rne(p) + rne(p - rne(p)): one alone costs a result of fp16 as
-    // much as its own rounding (4 bits: twice, as codes and minima are summed apart); to one of bf16 it adds 2 %
+    // much as its own rounding (4 bits: twice, as codes and minima are summed apart); to one of bf16 it adds 2 %.  The second
+    // costs half of the products again: 34 to 36 us for a cache of 146 MB, 140 to 163 us in tiles (64 GFLOP, a window).
     static constexpr int PARTS = BF16 ? 1 : 2;
     typedef Codes<FMT, D> C;
     h8 qf[NQ][KS];
@@ -629,9 +647,13 @@ struct Rows {
     }
 };
 
-// Few rows: a workgroup of W waves has the 16 * NQ rows of an item, and each wave every W-th block of tokens of its
-// piece.  A block's loads are under way while the one before is worked on: its keys are asked for as soon as the last
-// product with the keys before them has begun, scales and values likewise, so that they need no registers of their own.
+// Few rows: a workgroup of 4 waves has the 16 * NQ rows of an item, and each wave every 4th block of tokens of its piece.  A
+// block's loads are under way while the one before is worked on: its keys are asked for as soon as the last product with the
+// keys before them has begun, scales and values likewise, so that they need no registers of their own.
+//
+// Bound by bytes where many workgroups are resident (decode, 8 bits, 562 MB: 107 us), by a wave's own instructions where few
+// are: a block is some 800 of them, 4000 clocks, whatever the number of waves beside it (one sequence of 777 tokens, 8
+// heads: 11.0 us with 4 waves, 11.7 with 8; of 500 tokens 8.3 and 9.3).
 template <int FMT, int D, bool BF16, int NQ>
 __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel(AttnArgs a)
 {
@@ -838,17 +860,20 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
         }
 }
 
-// Many rows: a workgroup of eight waves has 16 * NQ rows of an item in each, and takes the blocks of its piece one by one.
-// Codes become fp16 operands once for all waves and lie in LDS in the order in which a wave reads them, 16 bytes a lane:
+// Many rows: a workgroup has kTileRows rows of an item, COLS in each of its W waves, and takes the blocks of its piece one by
+// one.  Codes become fp16 operands once for all waves and lie in LDS in the order in which a wave reads them, 16 bytes a lane:
 // no bank conflicts, and no permutation.
 //
-// A block is two phases of a wave: M, the products (of the block's keys, and of the values of the block before) and the
-// unpacking of what comes next, and S, the softmax.  One is bound by the matrix cores and the LDS, the other by the vector
-// units, and a SIMD has two of the waves: the second four run one phase behind the first, so that each SIMD has one wave in
-// either.  A barrier ends a phase.  With phases counted from 0, the first waves are in M(i) at 2 i and in S(i) at 2 i + 1,
-// the others one later; both write the keys of block i + 1 and the values of block i in M(i), which are read in M(i + 1),
-// from 2 i + 2 on, and lie where those of i - 1 and i - 2 did, last read in M(i - 1), at 2 i - 1.  Scales of block i + 1 go
-// along with its keys and are read in S(i + 1), 2 i + 3 and 2 i + 4: they take turns in four places.
+// A block is two phases of a wave: M, the products (of the values of the block before, and of the block's keys) with the
+// unpacking of what comes next between them, and S, the softmax.  One barrier a block stands between the two: what M(i)
+// writes (keys of block i + 1, values of block i) is read in M(i + 1), one barrier later, and lies where M(i - 1) read last,
+// one barrier earlier.  Scales of block i + 1 go along with its keys and are read in S(i + 1) by waves that may be one block
+// apart: they take turns in four places.
+//
+// Dims up to 128: 4 waves of 32 rows on 32x32x16, which reads half as much LDS a product as 16x16x32, and two workgroups a
+// compute unit, whose phases fall beside each other by themselves.  Against that, 8 waves of 16 rows of which four run a
+// phase behind the others by barriers were no faster at any case.  Dims of 256 fill the LDS with one workgroup: 8 waves of 16
+// rows (a chunk of 1024 tokens over 4096, 4 heads: 72 us; 4 waves of 32 rows, one on each SIMD: 89).
 template <int FMT, int D, bool BF16, int COLS, int W>
 __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attention_tile_kernel(AttnArgs a)
 {
@@ -939,7 +964,8 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
     auto unpack = [&](int op, int i) {
         const int q = op / PER % MINE, v = op % PER, chunk = wave + q * W;
         if (C::N % W != 0 && chunk >= C::N) return;
-        const int sj = lane >> 4, sr = lane & 15;        // the page's lane: 16 bytes of dims 16 sj of token sr, tokens 4 sj of dim sr
+        // the page's lane: 16 bytes of dims 16 sj of token sr, tokens 4 sj of dim sr
+        const int sj = lane >> 4, sr = lane & 15;
         if (op < OPS / 2) {
             const h8 f = C::key_of(kraw[q], v, mant);
             const int d = chunk % (D / 64), q0 = chunk / (D / 64) * (PER / 2) + v / 2;   // 64 dims, 16 tokens
@@ -1069,7 +1095,9 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
             if (i == 0) w.clear();                       // no values were there yet
             // the keys' scales before the barrier, the others as they are needed
             const float *ar = arrays + (i & 3) * 2 * A * 64 + 4 * j;
-            auto get = [ar](int which) { return [=](int q) { return *reinterpret_cast<const f4 *>(ar + which * 64 + 64 / QN * q); }; };
+            auto get = [ar](int which) {
+                return [=](int q) { return *reinterpret_cast<const f4 *>(ar + which * 64 + 64 / QN * q); };
+            };
             f4 ks[QN];
 #pragma unroll
             for (int q = 0; q < QN; ++q) ks[q] = get(0)(q);
@@ -1097,13 +1125,15 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
             f4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = ldexpf(w.o[0][i][4 * q + e] * inv, w.E - kTop) + add;
-            put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, w0 + n, COLS * i + 8 * q + 4 * j, v, w.mc[0], sum);
+            put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, w0 + n, COLS * i + 8 * q + 4 * j, v, w.mc[0],
+                                sum);
         }
 }
 
 // The pieces of a cut item's rows joined: each has its own normalised result, and weighs sum * 2^maximum.  The items of both
 // launches are joined by one, whose workgroups take `per` rows of an item and head at a time, dim / 4 lanes a row.  Where an
 // item has few pieces each row is the work of its own lanes; else rows come one by one, 256 / (dim / 4) pieces at a time.
+// 4 to 6 us, most of it the launch and four loads one after the other; 34 MB of pieces of tiles, 13 us.
 struct JoinArgs {
     AttnArgs a[2];                       // share = 0: nothing of it is cut
     int rows[2], per[2], groups[2], cuts[2];
@@ -1198,8 +1228,20 @@ __global__ __launch_bounds__(256, 6) void kv_attention_join_kernel(JoinArgs p)
 }
 
 constexpr int kTileRows = 128;
-constexpr int kWholeBlocks = 16;         // blocks up to which an item is not worth a second launch
-constexpr int64_t kFewBeside = 16;       // rows of a sequence up to which it goes with the few, where others have many
+// Blocks up to which an item is not worth a second launch: one sequence of 500 tokens, 8 heads of 128, 8 bits, takes 8.3 us
+// whole and 11.7 in pieces; of 1800 tokens, 17.0 and 10.8.
+constexpr int kWholeBlocks = 16;
+// Rows of a sequence up to which it goes with the few, where others have many: 1024 rows beside 31 sequences of one row, 4
+// heads of 256, take 118 us so, 178 all in tiles.
+constexpr int64_t kFewBeside = 16;
+// Rows of a sequence that the kernel for few takes: as many as its registers hold.  A tile does the products of 128 rows
+// whatever there are.  8 bits, sequences of up to 4001 tokens: 24 of 40 rows, 2 heads of 64, 22.2 us, 28.4 in tiles; 16 of 32
+// rows, 4 heads of 128, 23.6 and 36.4; 16 of 16 rows, 4 heads of 256, 26.1 and 39.8.
+int64_t few_rows(int dim) { return dim == 64 ? 64 : dim == 128 ? 32 : 16; }
+// Workgroups that are resident at once, which the pieces fill: two on a compute unit, one where LDS (tiles of 256 dims) or
+// registers (few rows, more than 128 sums a lane) leave room for no more.  Few rows, with the other of 256 and 512: 562 MB
+// 114.5 us for 120.5; 40 rows of 64 dims 22.2 for 28.3; tiles of 256 dims 118 for 134.
+int resident(int dim, int nq) { return dim * nq > 128 ? 256 : 512; }
 
 // A launch over the sequences of over < rows * group <= upto
 struct AttnPlan {
@@ -1212,14 +1254,14 @@ int64_t plan_bytes(const AttnPlan &p, const KvArgs &a)
 {
     if (p.share == 0) return 0;
     // 2 * share cut items have a place also where offsets that go back make more items than there are rows for
-    return p.slots * a.heads * p.rows * (a.dim * 4 + 8) + (2 * (int64_t)p.share + 1) * (int64_t)sizeof(int4);   // whole 16 bytes
+    return p.slots * a.heads * p.rows * (a.dim * 4 + 8) + (2 * (int64_t)p.share + 1) * (int64_t)sizeof(int4);
 }
-void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int resident)
+void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int places)
 {
     p.tiles = (int)((most_rows + p.rows - 1) / p.rows);
     const int64_t items = (int64_t)p.tiles * a.count, blocks = ((int64_t)a.width << a.page_shift) / kTile;
     const bool cut = items <= kMaxItems && blocks > kWholeBlocks;
-    p.share = cut ? std::max(resident / a.heads, 1) : 0;
+    p.share = cut ? std::max(places / a.heads, 1) : 0;
     // tiles that there can be: whole ones of all rows, and a sequence's last
     const int64_t there = std::min(items, (int64_t)a.rows * group / p.rows + std::min(a.count, a.rows));
     // T / size is at most 2 * share; a cut item has two pieces or more
@@ -1232,7 +1274,7 @@ void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int re
 int attn_plan(const KvArgs &a, int q_heads, AttnPlan *p)
 {
     const int group = q_heads / a.heads;
-    const int64_t rows = (int64_t)a.max_rows * group, few = a.dim == 64 ? 64 : a.dim == 128 ? 32 : 16;
+    const int64_t rows = (int64_t)a.max_rows * group, few = few_rows(a.dim);
     int n = 0;
     if (rows > few) {
         AttnPlan &t = p[n++];
@@ -1241,7 +1283,7 @@ int attn_plan(const KvArgs &a, int q_heads, AttnPlan *p)
         t.rows = kTileRows;
         t.over = a.count > 1 ? kFewBeside : 0;
         t.upto = INT64_MAX;
-        cut_plan(t, a, group, rows, a.dim == 256 ? 256 : 512);
+        cut_plan(t, a, group, rows, resident(a.dim, 1));
         if (a.count == 1) return n;
     }
     AttnPlan &f = p[n++];
@@ -1251,7 +1293,7 @@ int attn_plan(const KvArgs &a, int q_heads, AttnPlan *p)
     f.rows = 16 * f.nq;
     f.over = 0;
     f.upto = rows > few ? kFewBeside : INT64_MAX;
-    cut_plan(f, a, group, most, a.dim * f.nq > 128 ? 256 : 512);
+    cut_plan(f, a, group, most, resident(a.dim, f.nq));
     return n;
 }
 
@@ -1320,9 +1362,7 @@ hipError_t launch_kv_attention(const KvArgs &kv, const void *q, int64_t q_stride
             typedef std::integral_constant<int, 32> c32;
             typedef std::integral_constant<int, 4> w4;
             typedef std::integral_constant<int, 8> w8;
-            if constexpr (D == 256) {
-                e = tile(c16{}, w8{});
-            }
+            if constexpr (D == 256) e = tile(c16{}, w8{});
             else e = tile(c32{}, w4{});
         } else {
             auto few = [&](auto nq) {

@@ -170,8 +170,9 @@ def attention64(cache, batch, q, scale, window, dtype):
     Steps, relative to sums of magnitudes: the score's D products and their scale (D + 6 roundings of binary32, each
     dim at most |q| (|code scale| + |minimum|)); the exponent's two roundings of |score|; p and its sum (a few roundings
     each, the sum over at most n tokens); p * vscale to fp16 (half a step 2^-11 for results of bf16; for those of fp16 the
-    rest in a second part, and half a step of that: 2^-22; or half the spacing 2^-25 of what is near zero, in units of 2^(E - 6), E the exponent of the largest value scale that some row of the call sees); the
-    sum over tokens (n roundings); the joining of parts (a few roundings, one exp2 each, of 2^-22); the result's own."""
+    rest in a second part, and half a step of that: 2^-22; or half the spacing 2^-25 of what is near zero, in units of
+    2^(E - 6), E the exponent of the largest value scale that some row of the call sees); the sum over tokens (n
+    roundings); the joining of parts (a few roundings, one exp2 each, of 2^-22); the result's own."""
     rows, Hq, D = q.shape
     y, bound = np.zeros((batch.rows, Hq, D)), np.zeros((batch.rows, Hq, D))
     group = Hq // cache.heads

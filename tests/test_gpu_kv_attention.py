@@ -338,3 +338,82 @@ def test_head_layouts(heads, group):
     cache = filled(rng, "i8", 5, 64, heads, 64)
     for n in ([1, 1], [40, 2]):
         check(cache, Batch(cache, n, [100, 130], rng), group, "f16", rng, what=str(n))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_chunks_over_a_long_cache(fmt, D):
+    """Tiles cut into a few pieces and into many, beside sequences of few rows that are cut as well."""
+    rng = np.random.default_rng(22)
+    cache = filled(rng, fmt, 32, 256, 1, D)
+    check(cache, Batch(cache, [130], [1300], rng), 1, "f16", rng, what="few pieces")
+    check(cache, Batch(cache, [130, 1, 3, 0, 9], [4000, 2000, 700, 50, 200], rng), 2, "bf16", rng, what="many pieces")
+    check(cache, Batch(cache, [1, 40, 40], [1500, 2500, 3000], rng), 3, "f16", rng, window=1000, what="window")
+
+
+def many(cache, rng, B, longest, width):
+    """B sequences of few rows whose pages are any of the cache's."""
+    batch = Batch(cache, [int(x) for x in rng.integers(0, 3, B)], [0] * B, rng, width=width)
+    batch.lens = [int(x) for x in rng.integers(1, longest, B)]
+    batch.table = rng.integers(0, cache.pages, (B, width)).astype(np.int32)
+    return batch
+
+
+@pytest.mark.parametrize("B", [63, 64, 65, 511, 513])
+def test_many_sequences(B):
+    rng = np.random.default_rng(23)
+    cache = filled(rng, "i8", 20, 64, 1, 64)
+    check(cache, many(cache, rng, B, 1500 if B < 100 else 300, 24), 2, "bf16", rng)
+
+
+def test_offsets_that_go_back():
+    """Sequences that name the same rows again and again: nothing past the workspace or the rows is written."""
+    rng = np.random.default_rng(24)
+    cache = filled(rng, "i8", 20, 64, 1, 128)
+    B, rows_, Hq, D = 100, 150, 2, 128
+    batch = many(cache, rng, B, 1500, 24)
+    batch.rows, batch.max_rows = rows_, rows_
+    batch.offsets = np.where(np.arange(B + 1) % 2 == 0, 0, rows_).astype(np.int32)
+    handle = batch.device()
+    q = rows(rng, rows_, Hq, D, torch.bfloat16).cuda()
+    ch = cache.handle(cache.device())
+    need = lb.lowbit_kv_attention_workspace_bytes(ch, handle, Hq)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    y = torch.full((rows_ + 8, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lb.check(lb.lowbit_kv_attention(ch, handle, q, Hq * D, Hq, lb.LOWBIT_BF16, 0.1, 0, y, ws, need))
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0x5A).all() and (y[rows_:] == 7).all()
+
+
+def test_graphs_that_share_a_workspace():
+    """A chunk's graph and a decode step's, captured without a call before them, replayed in turn on one workspace."""
+    rng = np.random.default_rng(25)
+    heads, group, D = 2, 2, 256
+    Hq = heads * group
+    cache = filled(rng, "u4", 30, 128, heads, D)
+    data = cache.device()
+    stream, jobs = torch.cuda.Stream(), []
+    for n, lens in (([90, 1], [1500, 1100]), ([1, 1], [1200, 2000])):
+        batch = Batch(cache, n, lens, rng)
+        q = rows(rng, batch.rows, Hq, D, torch.float16)
+        jobs.append((batch, q, q.cuda(), batch.device(), torch.cuda.CUDAGraph(),
+                     torch.zeros((batch.rows, Hq, D), dtype=torch.float16, device="cuda")))
+    need = max(lb.lowbit_kv_attention_workspace_bytes(cache.handle(data), job[3], Hq) for job in jobs)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for batch, q, qd, h, graph, y in jobs:
+            with torch.cuda.graph(graph, stream=stream):
+                lb.check(lb.lowbit_kv_attention(cache.handle(data), h, qd, Hq * D, Hq, lb.LOWBIT_F16, 0.06, 0, y, ws, need,
+                                                stream.cuda_stream))
+        for turn in range(3):
+            for job in jobs:
+                job[5].fill_(float("nan"))
+            for job in jobs:
+                job[4].replay()
+            torch.cuda.synchronize()
+            for batch, q, qd, h, graph, y in jobs:
+                want, bound = attention64(cache, batch, q.double().numpy(), float(np.float32(0.06)), 0, torch.float16)
+                assert_within(y, want, bound, "turn %d" % turn)
+                eager = attend(cache.handle(data), batch, qd, Hq * D, Hq, "f16", 0.06, 0, batch.rows, D)
+                assert torch.equal(eager, y)
