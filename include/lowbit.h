@@ -694,7 +694,8 @@ typedef struct lowbit_kv_cache {
  *     page_size have no page: not written, read as zeros, not seen by attention;
  *   - a row that would stand before token 0 is not written, is read as zeros, and
  *     its attention is zeros, as is that of any row that sees no token;
- *   - offsets are cut to [0, rows]; rows of no sequence are left as they were.
+ *   - offsets are cut to [0, rows]; rows of no sequence are left as they were,
+ *     those that several sequences name (offsets that go back) are undefined.
  * A page may be shared by sequences that read it.  Where two rows of one
  * lowbit_kv_write stand for the same place of the same page, what the place
  * holds afterwards is undefined.
@@ -753,8 +754,8 @@ int lowbit_kv_read(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, v
  *   y         : [rows][q_heads * dim] of the same type (output), 16-byte aligned;
  *               must not overlap q
  *   workspace : >= lowbit_kv_attention_workspace_bytes(cache, batch, q_heads) bytes,
- *               256-byte aligned (partial results where few rows share out the
- *               tokens; may be NULL when that is 0).  Nothing in it outlives the
+ *               256-byte aligned (results of parts where a row's tokens are
+ *               shared out; may be NULL when that is 0).  Nothing in it outlives the
  *               call, and it needs no clearing; calls that may overlap need one each.
  */
 int lowbit_kv_attention(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, const void *q, int64_t q_stride,
