@@ -16,11 +16,11 @@
 // a time where the block is whole, by dwords and bytes at its ends: no byte of
 // another token is written.
 //
-// Both directions are bound by bytes.  8 bits, 8 heads of 128 dims: a prompt of
-// 16384 rows written and read back moves 2 x 101 MB in 25 + 18 us (its pages are
-// still in the last cache when they are read); 16 sequences read, 305 MB in 62
-// us, 4.9 TB/s.  32 rows of 32 sequences take 5 us, the launch and one round of
-// loads and stores.
+// Both directions are bound by bytes: 16 sequences of up to 8192 tokens read, 8
+// bits, 8 heads of 128 dims, move 305 MB in 59 us, 5.2 TB/s, as fast as a large
+// copy.  A prompt of 16384 rows, 102 MB, is written in 27 us and read back in 18
+// (its pages are still in the last cache then).  32 rows of 32 sequences take 5
+// us, the launch and one round of loads and stores.
 #include <cfloat>
 
 #include "kv_cache.hpp"
@@ -131,7 +131,7 @@ struct Share {
     __device__ __forceinline__ int dim(int ch) const { return ch * 128 + l * 8; }
 };
 
-template <int FMT, int D, bool BF16>
+template <int FMT, int D, bool BF16, bool PASSING>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, const uint16_t *k, int64_t k_stride,
                                                             const uint16_t *v, int64_t v_stride, int blocks)
 {
@@ -151,8 +151,10 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, const uint
 #pragma unroll
         for (int c = 0; c < S::CH; ++c) {
             raw[i][c] = us8{0, 0, 0, 0, 0, 0, 0, 0};
-            if (t >= o.lo && t < o.hi)
-                raw[i][c] = *reinterpret_cast<const us8 *>(src + (o.row + t) * stride + o.head * D + sh.dim(c));
+            if (t >= o.lo && t < o.hi) {
+                const us8 *at = reinterpret_cast<const us8 *>(src + (o.row + t) * stride + o.head * D + sh.dim(c));
+                raw[i][c] = PASSING ? __builtin_nontemporal_load(at) : *at;
+            }
         }
     }
     if (o.page < 0) return;
@@ -275,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, const uint
     }
 }
 
-template <int FMT, int D, bool BF16>
+template <int FMT, int D, bool BF16, bool PASSING>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, uint16_t *k, int64_t k_stride, uint16_t *v,
                                                            int64_t v_stride, int blocks)
 {
@@ -357,12 +359,20 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, uint16_t *k
                     out[e] = from_f32<BF16>(value);
                 }
             }
-            if (have) *reinterpret_cast<us8 *>(dst + (o.row + t) * stride + o.head * D + sh.dim(c)) = out;
+            if (!have) continue;
+            us8 *at = reinterpret_cast<us8 *>(dst + (o.row + t) * stride + o.head * D + sh.dim(c));
+            if constexpr (PASSING) __builtin_nontemporal_store(out, at);
+            else *at = out;
         }
     }
 }
 
-// A launch of KERNEL<FMT, D, BF16> for the sizes at hand
+// Rows of more bytes than the L2 caches hold go past them (nontemporal): a prompt of 16384 rows, 8 heads of 128 dims, 8 bits,
+// written and read back, 45.6 us for 50.6; 16 sequences of it read, 59 us for 66.  Few rows are in these caches, or wanted
+// there, by the products before and after: 10.1 us so for 9.5 (32 rows).
+constexpr int64_t kPassingBytes = 32 << 20;
+
+// A launch of KERNEL<FMT, D, BF16, PASSING> for the sizes at hand
 #define KV_LAUNCH(KERNEL, ...)                                                                      \
     do {                                                                                            \
         const int blocks = kv_blocks(a.max_rows);                                                   \
@@ -371,16 +381,21 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, uint16_t *k
             kernel<<<grid, kThreads, 0, s>>>(__VA_ARGS__, blocks);                                  \
             return hipGetLastError();                                                               \
         };                                                                                          \
-        auto dims = [&](auto fmt, auto bf) {                                                        \
+        auto dims = [&](auto fmt, auto bf, auto far) {                                              \
             constexpr int F = decltype(fmt)::value;                                                 \
-            constexpr bool B = decltype(bf)::value;                                                 \
-            return a.dim == 64 ? go(KERNEL<F, 64, B>)                                               \
-                               : a.dim == 128 ? go(KERNEL<F, 128, B>) : go(KERNEL<F, 256, B>);      \
+            constexpr bool B = decltype(bf)::value, P = decltype(far)::value;                       \
+            return a.dim == 64 ? go(KERNEL<F, 64, B, P>)                                            \
+                               : a.dim == 128 ? go(KERNEL<F, 128, B, P>) : go(KERNEL<F, 256, B, P>);\
         };                                                                                          \
-        using i8 = std::integral_constant<int, LOWBIT_KV_I8>;                                       \
-        using u4b = std::integral_constant<int, LOWBIT_KV_U4>;                                      \
-        if (a.fmt == LOWBIT_KV_I8) return bf16 ? dims(i8{}, std::true_type{}) : dims(i8{}, std::false_type{});  \
-        return bf16 ? dims(u4b{}, std::true_type{}) : dims(u4b{}, std::false_type{});               \
+        auto types = [&](auto fmt, auto far) {                                                      \
+            return bf16 ? dims(fmt, std::true_type{}, far) : dims(fmt, std::false_type{}, far);     \
+        };                                                                                          \
+        auto formats = [&](auto far) {                                                              \
+            return a.fmt == LOWBIT_KV_I8 ? types(std::integral_constant<int, LOWBIT_KV_I8>{}, far)  \
+                                         : types(std::integral_constant<int, LOWBIT_KV_U4>{}, far); \
+        };                                                                                          \
+        const bool passing = (int64_t)a.rows * a.heads * a.dim * 4 > kPassingBytes;                 \
+        return passing ? formats(std::true_type{}) : formats(std::false_type{});                    \
     } while (0)
 
 }  // namespace

@@ -241,3 +241,40 @@ def test_graph_replays_with_new_lengths(fmt):
             step = x.abs().amax(-1) / 254 if fmt == "i8" else (x.amax(-1) - x.amin(-1)) / 30
             off = (got[:total].cpu().float() - x).abs().amax(-1)
             assert (off <= step * 1.01 + 2.0 ** -10 * x.abs().amax(-1)).all()
+
+
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_long_prompt_at_once_and_in_parts(fmt):
+    """Rows of more than 32 MB in one call, and the same in calls of a few hundred: equal bytes, equal rows."""
+    rng = np.random.default_rng(31)
+    heads, D, page, total = 20, 128, 128, 3333
+    assert total * heads * D * 4 > 32 << 20
+    cache = Cache(fmt, 30, page, heads, D)
+    k, v = (torch.randn((total, heads, D), device="cuda").to(torch.bfloat16) for _ in range(2))
+    k[5, 3, 100] = float("inf")
+    table = rng.permutation(30).astype(np.int32)
+    stride, datas, outs = heads * D, [], []
+    for step in (total, 700):
+        data = torch.full(cache.b.shape, 0x55, dtype=torch.uint8, device="cuda")
+        back = [torch.zeros((total, heads, D), dtype=torch.float16, device="cuda") for _ in range(2)]
+        for call, x, y in ((lb.lowbit_kv_write, (k, v), lb.LOWBIT_BF16), (lb.lowbit_kv_read, back, lb.LOWBIT_F16)):
+            for at in range(0, total, step):
+                n = min(step, total - at)
+                batch = Batch(cache, [n], [at + n], rng, width=27)
+                batch.table[0] = table[:27]
+                lb.check(call(cache.handle(data), batch.device(), x[0][at:].data_ptr(), stride, x[1][at:].data_ptr(),
+                              stride, y))
+        torch.cuda.synchronize()
+        datas.append(data)
+        outs.append(back)
+    assert torch.equal(datas[0], datas[1])
+    for a, b in zip(*outs):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    # 8 bits: half a step of amax / 127; 4: of the row's range / 15; the fp16 rounding is far below either's margin of 2 %
+    step = (lambda x: x.amax(-1) - x.amin(-1)) if fmt == "u4" else (lambda x: x.abs().amax(-1))
+    for x, y in ((k, outs[0][0]), (v, outs[0][1])):
+        x = x.float()
+        half = step(x) / (15 if fmt == "u4" else 127) / 2
+        good = torch.isfinite(x).all(-1)
+        assert ((x - y.float()).abs().amax(-1) <= half * 1.02 + 2.0 ** -9)[good].all()
+        assert torch.isnan(y[~good]).all() and int((~good).sum()) == (1 if x.isinf().any() else 0)
