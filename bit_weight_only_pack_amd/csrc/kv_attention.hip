@@ -26,8 +26,8 @@
 // and its bytes are the bound: 562 MB of 8 bit cache for one token each of 64
 // sequences of up to 8192 in 107 us, 5.2 TB/s, as fast as a large copy.  Many rows
 // (kv_attention_tile_kernel) are bound by the instructions of a compute unit,
-// matrix and vector ones: 515 GFLOP of a causal prompt in 0.61 ms, 845 TFLOP/s,
-// 70 % of a large library product's rate.
+// matrix and vector ones: 515 GFLOP of a causal prompt in 0.57 ms, 900 TFLOP/s,
+// 74 % of a large library product's rate.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
