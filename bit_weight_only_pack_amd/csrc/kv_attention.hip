@@ -163,7 +163,8 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, int rows, int want
     total = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)total, plus), 63);
     most = __builtin_amdgcn_readlane(wave_scan(most, larger), 63);
     const int wanted = a.fill ? (there / 2 / a.share + 1) * a.share - there / 2 : there > a.share / 2 ? 2 * a.share : a.share;
-    const int even = max((int)((((int64_t)total << 2) + wanted - 1) / wanted), kMinPiece);
+    const int64_t share = (((int64_t)total << 2) + wanted - 1) / wanted;
+    const int even = (int)min(max(share, (int64_t)kMinPiece), (int64_t)1 << 25);     // past any item's blocks
     o.size = __builtin_amdgcn_readfirstlane(most <= even + even / 2 ? max(most, 1) : even);
     int before = 0, slots = 0;
     o.cuts = 0;
