@@ -295,6 +295,13 @@ __device__ __forceinline__ bool inside(int at, int lo, int hi) { return (at >= l
 __device__ __forceinline__ float finite_max(float top, float v) { return fabsf(v) <= FLT_MAX ? fmaxf(top, fabsf(v)) : top; }
 
 // largest over the four lanes of a column (l, l ^ 16, l ^ 32, l ^ 48): swaps of lane rows, no LDS
+__device__ __forceinline__ uint32_t column_max(uint32_t v)
+{
+    auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(p[0], p[1]);
+    p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max(p[0], p[1]);
+}
 __device__ __forceinline__ float column_max(float v)
 {
     auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -746,23 +753,23 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
                 for (int e = 0; e < 4; ++e)
                     r.vs[q][e] = inside(16 * q + 4 * j + e, lo, hi) ? r.vs[q][e] : 0.f;
         }
-        // value scales: the largest exponent so far, infinities and NaN aside
-        float v_top = 0.f;
+        // value scales: the largest exponent so far, infinities and NaN aside.  As bits: those of what is negative or no finite
+        // number are above all others, and no comparison quiets what was loaded first.
+        uint32_t v_top = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; e += 2)       // as fmaxf would, without quieting what was loaded first
-                asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(v_top) : "v"(r.vs[q][e]), "v"(r.vs[q][e + 1]));
+            for (int e = 0; e < 4; ++e) v_top = max(v_top, __float_as_uint(r.vs[q][e]));
         v_top = column_max(v_top);
-        if ((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >= 0x7f800000u) {
-            v_top = 0.f;
+        if ((uint32_t)__builtin_amdgcn_readfirstlane(v_top) >= 0x7f800000u) {
+            float top = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v_top = finite_max(v_top, r.vs[q][e]);
-            v_top = column_max(v_top);
+                for (int e = 0; e < 4; ++e) top = finite_max(top, r.vs[q][e]);
+            v_top = __float_as_uint(column_max(top));
         }
-        w.move_to(max((int)((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >> 23) - 127, w.E));
+        w.move_to(max((int)((uint32_t)__builtin_amdgcn_readfirstlane(v_top) >> 23) - 127, w.E));
         const float norm = ldexpf(1.f, kTop - w.E);
 #pragma unroll
         for (int q = 0; q < 4; ++q) r.vs[q] *= norm;

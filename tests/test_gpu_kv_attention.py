@@ -179,6 +179,21 @@ def test_scales_of_all_sizes(fmt):
         assert torch.isnan(y[1, 0]).all() and torch.isfinite(y[1, 1:]).all() and torch.isfinite(y[0]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_scales_of_either_sign(fmt, D):
+    """A value is code * scale (+ minimum), also where a page that the caller made has a negative scale."""
+    rng = np.random.default_rng(26)
+    cache = filled(rng, fmt, 12, 64, 1, D)
+    for i in range(2):
+        cache.meta(i, 0)[:] *= rng.choice(np.array([-1, 1], np.float32), (12, 1, 64))
+        cache.meta(i, 0)[3] = -np.abs(cache.meta(i, 0)[3])
+    for n in ([1, 2, 0], [33, 90, 1]):
+        batch = Batch(cache, n, [200, 230, 64], rng)
+        batch.table[0, 1], batch.table[1, 2] = 3, 3                    # a block of negative scales alone
+        check(cache, batch, 2, "f16", rng, what=str(n))
+
+
 @pytest.mark.parametrize("fmt", ["i8", "u4"])
 def test_one_token_far_above_the_rest(fmt):
     """A softmax of one token's weight, first, in the middle and last."""
