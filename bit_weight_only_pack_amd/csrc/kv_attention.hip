@@ -15,7 +15,8 @@
 // Scales stand outside of the sums over dims (keys) and inside of those over
 // tokens (values): s = kscale * acc (+ kmin * sum of q, 4 bits), and the fp16
 // operand is p * vscale * 2^(kTop - E), E the largest exponent of a value scale
-// so far.  The minima of values enter as sum p * vmin, one number per row.  The
+// so far; where scales differ by more than 2^8 (bf16 results: 2^14), each row
+// takes its operands to the largest of its own instead (Rows::SPREAD).  The minima of values enter as sum p * vmin, one number per row.  The
 // softmax runs in one pass; the maximum that a row's terms are taken to moves
 // only where one passes it by 2^kSlack, so that most blocks rescale nothing.
 // The operand stays under 2^(kSlack + kTop + 1) = 2^15, and terms down to 2^-20 of
@@ -291,17 +292,7 @@ struct Codes {
 
 __device__ __forceinline__ bool inside(int at, int lo, int hi) { return (at >= lo) & (at < hi); }
 
-// the larger of `top` and |v|, if v is finite
-__device__ __forceinline__ float finite_max(float top, float v) { return fabsf(v) <= FLT_MAX ? fmaxf(top, fabsf(v)) : top; }
-
 // largest over the four lanes of a column (l, l ^ 16, l ^ 32, l ^ 48): swaps of lane rows, no LDS
-__device__ __forceinline__ uint32_t column_max(uint32_t v)
-{
-    auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    v = max(p[0], p[1]);
-    p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return max(p[0], p[1]);
-}
 __device__ __forceinline__ float column_max(float v)
 {
     auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -309,10 +300,30 @@ __device__ __forceinline__ float column_max(float v)
     p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
-template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v)
+// Exponent fields of the largest and the smallest number of a set, the latter as 255 less itself: halves of a dword, so that
+// one maximum serves for both.  0: no number.
+__device__ __forceinline__ uint32_t range_max(uint32_t a, uint32_t b)
 {
-    return fmaxf(v, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xf, 0xf, true)));
+    typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
+}
+__device__ __forceinline__ uint32_t column_range(uint32_t v)
+{
+    auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = range_max(p[0], p[1]);
+    p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return range_max(p[0], p[1]);
+}
+// of |v|, if v is finite
+__device__ __forceinline__ uint32_t range_of(float v)
+{
+    const uint32_t e = __float_as_uint(v) >> 23 & 255u;
+    return e == 255u ? 0u : e | (255u - e) << 16;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_range(uint32_t v)
+{
+    return range_max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true));
 }
 __device__ __forceinline__ float column_sum(float v)
 {
@@ -362,6 +373,16 @@ struct BlockRegs {
 // p <= 2^kSlack, and the operand p * vscale * 2^(kTop - E) stays below 2^15.
 constexpr float kSlack = 8.f;
 constexpr int kTop = 6;
+
+// Exponents of the value scales that some row of the item has seen: the largest and the smallest (0 has -127)
+struct ValueRange {
+    int top = -100, low = 128;
+    __device__ __forceinline__ void join(uint32_t range)     // of a whole wave: exponent fields as above
+    {
+        top = max(top, (int)(range & 0xffffu) - 127);
+        low = min(low, 128 - (int)(range >> 16));
+    }
+};
 
 // How a matrix instruction lays things out: COLS = 16 (16x16x32) or 32 (32x32x16) rows of the item are its columns; a lane
 // l has column l % COLS and, j being l / COLS, the tokens (64 / QN) * q + 4 j + e of a block, q < QN and e < 4, and as many
@@ -417,6 +438,13 @@ struct Rows {
     float mc[NQ], limit[NQ];             // exponent that the row's terms are taken to, and what they may pass it by
     float l[NQ], bias[NQ];               // sums of the lane's p and p * vmin
     int E;
+    // Where the item's value scales spread by more than this, the row's own tokens may have small ones, or those that count
+    // for much: its sums are then taken to the largest p * vscale so far, by 2^k more than to E.  Up to here the largest
+    // operand is at least 2^(kTop - SPREAD), 2^23 (bf16 results: 2^17) times what fp16 rounds next to zero.
+    static constexpr int SPREAD = BF16 ? 14 : 8;
+    static constexpr int NONE = 1 << 20; // k of a row that has no sums yet
+    bool spread;
+    int k[NQ];
 
     // first of the 8 dims that lanes j have in step k
     static __device__ __forceinline__ int dims(int k, int j)
@@ -450,7 +478,8 @@ struct Rows {
         int top[NQ];                     // largest |q| of the row, its bits; 0 where there is none or no number
         float all = a.scale2;
         alike = true;
-        E = -100;
+        E = ValueRange().top;
+        spread = false;
         clear();
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
@@ -462,6 +491,7 @@ struct Rows {
             for (int k = 0; k < KS; ++k) raw[x][k] = *reinterpret_cast<const us8 *>(src + dims(k, j));
             c[x] = EVEN ? 1.f : a.scale2;
             qsum[x] = l[x] = bias[x] = mc[x] = 0.f;
+            k[x] = 0;
             limit[x] = -INFINITY;
             if constexpr (BF16) {
                 top[x] = 0;
@@ -520,24 +550,38 @@ struct Rows {
         return fminf(fmaxf(all, FLT_MIN), FLT_MAX);
     }
 
-    // takes the sums to another exponent of the value scales
-    __device__ __forceinline__ void move_to(int e)
+    // takes the sums to the exponents of the value scales as they are now: what they are to be multiplied by goes to `down`;
+    // returns whether that may be other than 1
+    __device__ __forceinline__ bool move_to(const ValueRange &range, float (&down)[NQ])
     {
-        if (e == E) return;
-        const float f = ldexpf(1.f, E - e);
+        if (!spread && range.top - range.low > SPREAD) {
+            spread = true;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) scale_sums(x, f);
-        E = e;
+            for (int x = 0; x < NQ; ++x) k[x] = limit[x] == -INFINITY ? NONE : 0;
+        }
+        const int by = range.top - E;
+        const float f = spread ? 1.f : ldexpf(1.f, -by);
+        E = range.top;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            k[x] = spread ? min(k[x] + by, NONE) : 0;
+            down[x] = f;
+        }
+        return spread | (by != 0);
     }
+    // what a sum is to be multiplied by, as an exponent
+    __device__ __forceinline__ int unit(int x) const { return E - kTop - k[x]; }
 
     // acc: products of the queries with a block's codes; leaves the operand of the product with its values.  kl, vl (4
     // bits): minima + 8 scales (the keys' with the factor of their scales); vs: times 2^(kTop - E).
     // masked: some row does not see all of the block, whose first token is t0, or its page is missing.
     template <typename KS_, typename KL, typename VS, typename VL>
     __device__ __forceinline__ void weigh(Acc (&acc)[NQ][S::TILES], KS_ ks, KL kl, VS vs, VL vl, bool masked, bool paged,
-                                          int64_t t0, int j, h8 (&pf)[PARTS][NQ][PU])
+                                          int64_t t0, int j, const ValueRange &range, h8 (&pf)[PARTS][NQ][PU])
     {
         constexpr int T = 64 / QN;       // tokens from one q to the next
+        float down[NQ];                  // what the sums so far are multiplied by, once, at the end
+        bool move = move_to(range, down);
         auto s = [&](int x, int q, int e) -> float { return acc[x][q * 4 / EL][q * 4 % EL + e]; };
         auto put = [&](int x, int q, int e, float v) { acc[x][q * 4 / EL][q * 4 % EL + e] = v; };
         // exponents, less the one that the row's terms are taken to
@@ -588,23 +632,27 @@ struct Rows {
             far |= top[x] > limit[x];
         }
         // the exponent moves where a row's first token is seen, and where one has passed it by more than the slack
-        if (__any(far))
+        if (__any(far)) {
+            move = true;
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
                 const float t = S::max_of(top[x]);
+                // a whole number, so that what was summed up is taken to it exactly
                 const bool none = limit[x] == -INFINITY;
-                const float to = t == -INFINITY ? mc[x] : mc[x] + (none ? t : fmaxf(t, 0.f));
+                const float to = t == -INFINITY ? mc[x] : mc[x] + (none ? floorf(t) : fmaxf(floorf(t), 0.f));
                 const float by = to - mc[x], alpha = none ? 0.f : exp2_fast(-by);
                 mc[x] = to;
                 limit[x] = t == -INFINITY ? limit[x] : kSlack;
                 l[x] *= alpha;
                 bias[x] *= alpha;
-                scale_sums(x, alpha);
+                down[x] *= spread ? 1.f : alpha;
+                k[x] = spread ? min(k[x] + (int)fminf(by, (float)NONE), NONE) : 0;
 #pragma unroll
                 for (int q = 0; q < QN; ++q)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) put(x, q, e, s(x, q, e) - by);
             }
+        }
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             float sum[2] = {0.f, 0.f};
@@ -645,6 +693,27 @@ struct Rows {
                     }
             }
         }
+        if (spread)
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                float t = 0.f;
+#pragma unroll
+                for (int q = 0; q < QN; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t = fmaxf(t, fabsf(s(x, q, e)));
+                t = S::max_of(t);
+                const int at = (int)(__float_as_uint(t) >> 23) - 127;
+                const int to = t > 0.f && t <= FLT_MAX && at + k[x] > 14 ? min(max(kTop - at, 0), E + 100) : k[x];
+                down[x] *= ldexpf(1.f, to - k[x]);
+                k[x] = to;
+#pragma unroll
+                for (int q = 0; q < QN; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) put(x, q, e, ldexpf(s(x, q, e), k[x]));
+            }
+        if (move)
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) scale_sums(x, down[x]);
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
 #pragma unroll
@@ -674,7 +743,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
     typedef Codes<FMT, D> C;
     __shared__ __attribute__((aligned(16))) float o_s[W * 16 * LD];
     __shared__ float m_s[NQ][W][16], l_s[NQ][W][16], b_s[NQ][W][16];
-    __shared__ int e_s[W];
+    __shared__ int e_s[NQ][W][16];
     __shared__ float g_s[NQ][W][16], add_s[NQ][16], top_s[NQ][16], sum_s[NQ][16];
 
     const int kvh = a.by_heads.rest(blockIdx.x), number = a.by_heads.of(blockIdx.x);
@@ -712,6 +781,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
     auto part_of = [&](int p) { return buffer_rsrc(kv_part(a.kv, max(p, 0), kvh), a.kv.part); };
     uint32_t mant = 0x64006400u;
     asm("" : "+v"(mant));
+    ValueRange values;
 
     // `more`: another block follows
     auto step = [&](auto more, __amdgpu_buffer_rsrc_t part, int next_at) {
@@ -744,38 +814,47 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
         const int64_t t0 = (int64_t)blk * kTile;
         // some row does not see all of the block
         const bool masked = page < 0 || blk < (t.seen_lo + kTile - 1) / kTile || blk >= t.seen_hi / kTile;
+        // value scales: their range, by their bits, as numbers of either sign and those that are not finite lie above all others
+        uint32_t v_top = 0, v_low = ~0u;
         if (masked) {
             // tokens that no row sees: their scales do not count
             const int lo = (int)max((int64_t)0, t.lo - t0), hi = page < 0 ? 0 : (int)min((int64_t)kTile, t.hi - t0);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    r.vs[q][e] = inside(16 * q + 4 * j + e, lo, hi) ? r.vs[q][e] : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    const bool seen = inside(16 * q + 4 * j + e, lo, hi);
+                    v_low = min(v_low, seen ? __float_as_uint(r.vs[q][e]) : ~0u);
+                    r.vs[q][e] = seen ? r.vs[q][e] : 0.f;
+                }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v_low = min(v_low, __float_as_uint(r.vs[q][e]));
         }
-        // value scales: the largest exponent so far, infinities and NaN aside.  As bits: those of what is negative or no finite
-        // number are above all others, and no comparison quiets what was loaded first.
-        uint32_t v_top = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v_top = max(v_top, __float_as_uint(r.vs[q][e]));
-        v_top = column_max(v_top);
-        if ((uint32_t)__builtin_amdgcn_readfirstlane(v_top) >= 0x7f800000u) {
-            float top = 0.f;
+        uint32_t range = __builtin_amdgcn_readfirstlane(column_range(v_top >> 23 | (255u - min(v_low >> 23, 255u)) << 16));
+        if ((range & 0xffffu) >= 255u) {
+            // one by one; those that no row sees are 0 by now, and make a wide range of it
+            range = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = finite_max(top, r.vs[q][e]);
-            v_top = __float_as_uint(column_max(top));
+                for (int e = 0; e < 4; ++e) range = range_max(range, range_of(r.vs[q][e]));
+            range = __builtin_amdgcn_readfirstlane(column_range(range));
         }
-        w.move_to(max((int)((uint32_t)__builtin_amdgcn_readfirstlane(v_top) >> 23) - 127, w.E));
-        const float norm = ldexpf(1.f, kTop - w.E);
+        values.join(range);
+        const float norm = ldexpf(1.f, kTop - values.top);
 #pragma unroll
         for (int q = 0; q < 4; ++q) r.vs[q] *= norm;
         h8 pf[PARTS][NQ][2];
         auto of = [](const f4 *v) { return [v](int q) { return v[q]; }; };
-        w.weigh(s, of(r.ks), of(r.kl), of(r.vs), of(r.vl), masked, page >= 0, t0, j, pf);
+        w.weigh(s, of(r.ks), of(r.kl), of(r.vs), of(r.vl), masked, page >= 0, t0, j, values,
+                pf);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MORE) r.load_arrays(part, next_at, j, page_size);
         __builtin_amdgcn_sched_barrier(0);
@@ -821,9 +900,9 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
             m_s[x][wave][n] = w.mc[x];
             l_s[x][wave][n] = w.l[x];
             b_s[x][wave][n] = w.bias[x];
+            e_s[x][wave][n] = w.unit(x);
         }
     }
-    if (lane == 0) e_s[wave] = w.E - kTop;
     __syncthreads();
     if (threadIdx.x < ROWS) {
         const int x = threadIdx.x / 16, row = threadIdx.x % 16;
@@ -839,7 +918,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
 #pragma unroll
         for (int q = 0; q < W; ++q) {
             add += f[q] == 0.f ? 0.f : b_s[x][q][row] * (f[q] * inv);
-            g_s[x][q][row] = ldexpf(f[q] * inv, e_s[q]);
+            g_s[x][q][row] = ldexpf(f[q] * inv, e_s[x][q][row]);
         }
         add_s[x][row] = add;
         top_s[x][row] = top;
@@ -995,11 +1074,13 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
                         h4{f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]};
         }
     };
-    // Scales of a block on their way to LDS, a token a lane.  Every wave has all of them: the largest exponent of the value
-    // scales so far (of tokens that some row sees, infinities and NaN aside) is the same in each, and comes about in steps
-    // that fit between products.
-    float scale[2], low[2], v_top;
-    int v_exp = -100, page_a = -1;
+    // Scales of a block on their way to LDS, a token a lane.  Every wave has all of them: the range of the value scales so far
+    // (of tokens that some row sees, infinities and NaN aside) is the same in each, and comes about in steps that fit between
+    // products.
+    float scale[2], low[2];
+    uint32_t v_range;
+    ValueRange values;
+    int page_a = -1;
     auto fetch_scales = [&](int blk) {   // of blk, whose page is page_k
         page_a = page_k;
         const auto part = part_of(page_k);
@@ -1016,15 +1097,14 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
     auto unpack_scales = [&](int step, int i) {
         if (step == 0) {
             const int64_t token = (int64_t)(begin + i) * kTile + lane;
-            v_top = ((token >= t.lo) & (token < t.hi) & (page_a >= 0)) ? finite_max(0.f, scale[1]) : 0.f;
+            v_range = ((token >= t.lo) & (token < t.hi) & (page_a >= 0)) ? range_of(scale[1]) : 0u;
         }
-        if (step == 1) v_top = dpp_max<0xb1>(v_top);
-        if (step == 2) v_top = dpp_max<0x4e>(v_top);
-        if (step == 3) v_top = dpp_max<0x141>(v_top);
-        if (step == 4) v_top = dpp_max<0x140>(v_top);
-        if (step == 5) v_top = column_max(v_top);
-        if (step == 6)
-            v_exp = max(v_exp, (int)((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v_top)) >> 23) - 127);
+        if (step == 1) v_range = dpp_range<0xb1>(v_range);
+        if (step == 2) v_range = dpp_range<0x4e>(v_range);
+        if (step == 3) v_range = dpp_range<0x141>(v_range);
+        if (step == 4) v_range = dpp_range<0x140>(v_range);
+        if (step == 5) v_range = column_range(v_range);
+        if (step == 6) values.join(__builtin_amdgcn_readfirstlane(v_range));
         if (step == 7) {
             float *at = arrays + (i & 3) * 2 * A * 64 + lane;
             if (wave == 0) {
@@ -1032,7 +1112,7 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
                 if constexpr (!I8) at[64] = __builtin_fmaf(8.f, scale[0], low[0]) * k_factor;
             }
             if (wave == 1) {
-                at[A * 64] = ldexpf(scale[1], kTop - v_exp);
+                at[A * 64] = ldexpf(scale[1], kTop - values.top);
                 if constexpr (!I8) at[3 * 64] = __builtin_fmaf(8.f, scale[1], low[1]);
             }
         }
@@ -1099,7 +1179,8 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
         __syncthreads();
         for (int i = 0; i < count; ++i) {
             // M
-            const int page = page_next, e_now = v_exp, blk = begin + i;
+            const int page = page_next, blk = begin + i;
+            const ValueRange now = values;
             page_next = page_k;
             __builtin_amdgcn_s_setprio(1);
             multiply(std::true_type{}, i);
@@ -1117,8 +1198,8 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
             // S
             if (wn > 0 && blk >= ws.first && blk < ws.end && page >= 0) {
                 const bool masked = blk < (ws.seen_lo + kTile - 1) / kTile || blk >= ws.seen_hi / kTile;
-                w.move_to(e_now);
-                w.weigh(s, [&](int q) { return ks[q]; }, get(1), get(A), get(3), masked, true, (int64_t)blk * kTile, j, pf);
+                w.weigh(s, [&](int q) { return ks[q]; }, get(1), get(A), get(3), masked, true, (int64_t)blk * kTile, j,
+                        now, pf);
             } else {
                 no_weights();
             }
@@ -1135,7 +1216,7 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
         for (int q = 0; q < R::EL / 4; ++q) {
             f4 v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = ldexpf(w.o[0][i][4 * q + e] * inv, w.E - kTop) + add;
+            for (int e = 0; e < 4; ++e) v[e] = ldexpf(w.o[0][i][4 * q + e] * inv, w.unit(0)) + add;
             put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, w0 + n, COLS * i + 8 * q + 4 * j, v, w.mc[0],
                                 sum);
         }

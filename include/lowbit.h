@@ -742,9 +742,12 @@ int lowbit_kv_read(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, v
  * that row r stands for; group = q_heads / heads; k and v are the values that the
  * cache holds.  One entry point for single tokens, drafted tokens and prompts;
  * the rows of the call have been written before (lowbit_kv_write).
- * Sums, maxima and the softmax are held in fp32; for the matrix cores p goes to
- * fp16 (fp16 results: to two fp16 parts, good for 22 bits), and q too if it is
- * bf16, after a power of two: values below 2^-20 of their row's largest lose bits.
+ * Sums, maxima and the softmax are held in fp32.  For the matrix cores p times the
+ * scale of the value goes to fp16 (fp16 results: to two fp16 parts, good for 22
+ * bits) after a power of two: it is off by half a step, or by 2^-23 (bf16 results:
+ * 2^-17) of the row's largest such product.  So does q if it is bf16: what is below
+ * 2^-31 of its row's largest counts for nothing, as do weights below 2^-100 of the
+ * row's largest.
  *   q         : [rows] rows of q_heads * dim values, LOWBIT_F16 or LOWBIT_BF16,
  *               16-byte aligned, q_stride values apart (at least q_heads * dim, a
  *               multiple of 8)
