@@ -891,7 +891,8 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
         step(std::false_type{}, part_of(page), 0);
     }
 
-    // the waves' results joined: what each counts for in a row, then 16 rows and up to 128 dims at a time
+    // the waves' results joined: what each counts for in a row, then 16 rows and up to 128 dims at a time.  One that saw
+    // nothing has sums of 0; one whose weight is 0 beside the others' still makes NaN of a row that sees NaN there
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
         w.l[x] = column_sum(w.l[x]);
@@ -917,7 +918,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-            add += f[q] == 0.f ? 0.f : b_s[x][q][row] * (f[q] * inv);
+            add += b_s[x][q][row] * (f[q] * inv);
             g_s[x][q][row] = ldexpf(f[q] * inv, e_s[x][q][row]);
         }
         add_s[x][row] = add;
@@ -942,7 +943,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
                     const float g = g_s[x][q][row];
                     const f4 ow = *reinterpret_cast<const f4 *>(o_s + (q * 16 + row) * LD + d);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = g == 0.f ? v[e] : __builtin_fmaf(ow[e], g, v[e]);
+                    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(ow[e], g, v[e]);
                 }
                 put_result<D, BF16>(a, t, pc.count, pc.slot + pc.piece, kvh, ROWS, 16 * x + row, d0 + d, v, top_s[x][row],
                                     sum_s[x][row]);

@@ -347,6 +347,27 @@ def test_pages_shared_between_sequences():
     check(cache, batch, 4, "bf16", rng)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_nan_of_no_weight(fmt, D):
+    """A row that sees a token of NaN is NaN, whatever that token weighs and wherever it lies beside those that do."""
+    rng = np.random.default_rng(27)
+    cache = filled(rng, fmt, 50 if D == 64 else 12, 64, 1, D)
+    q = torch.ones((200, 1, D), dtype=torch.float16)
+    for length, n in ((300, 1), (300, 90)) + (((3000, 1), (3000, 90)) if D == 64 else ()):
+        batch = Batch(cache, [n], [length], rng)
+        for at, which in ((10, 0), (70, 0), (150, 0), (length - n, 0)) + (((130, 1),) if fmt == "u4" else ()):
+            for heavy in (0, 100, 200):
+                b = cache.b.copy()
+                cache.put(0, *batch.where(cache, 0, np.array([heavy])), 0, np.full((1, D), 120 / D ** 0.5, np.float32))
+                page, t = batch.where(cache, 0, np.array([at]))
+                cache.put(0, page, t, 0, np.full((1, D), -120 / D ** 0.5, np.float32))
+                cache.meta(1, which)[page, 0, t] = np.nan
+                y = check(cache, batch, 1, "f16", rng, q=q[:n])
+                assert torch.isnan(y).all(), (length, n, at, which, heavy)
+                cache.b = b
+
+
 @pytest.mark.parametrize("heads,group", [(1, 1), (1, 64), (5, 3), (7, 1), (16, 2), (32, 1)])
 def test_head_layouts(heads, group):
     rng = np.random.default_rng(heads * 100 + group)
