@@ -75,7 +75,7 @@ struct AttnArgs {
     int64_t over, upto;                  // sequences of over < n * group <= upto rows are this launch's
     int share, fill;                     // 0: a workgroup takes an item's tokens whole; else how many pieces to make of all
     float *part_o;                       // [slots][heads][rows][dim]
-    float2 *part_ml;                     // [slots][heads][rows]: maximum and sum of each row's softmax
+    float2 *part_ml;                     // [slots][heads][rows]: exponent and sum of each row's softmax
     int4 *cuts;                          // [0]: how many items are cut; then item, first slot and pieces of each
 };
 
@@ -205,22 +205,6 @@ __device__ __forceinline__ uint16_t round_out(float v)
 }
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
-
-// 4 dims of a finished row: into y where its item is one piece, else among the pieces' results
-template <int D, bool BF16>
-__device__ __forceinline__ void put_result(const AttnArgs &a, const Span &t, int pieces, int slot, int kvh, int rows,
-                                           int rr, int d, f4 v, float top, float sum)
-{
-    if (pieces == 1) {
-        const int r = t.r0 + rr, i = a.by_group.of(r), h = a.by_group.rest(r);
-        const ushort4 w = {round_out<BF16>(v[0]), round_out<BF16>(v[1]), round_out<BF16>(v[2]), round_out<BF16>(v[3])};
-        *reinterpret_cast<ushort4 *>(a.y + ((int64_t)(t.s.row0 + i) * a.q_heads + kvh * a.group + h) * D + d) = w;
-    } else {
-        const int64_t p = ((int64_t)slot * a.kv.heads + kvh) * rows + rr;
-        *reinterpret_cast<f4 *>(a.part_o + p * D + d) = v;
-        if (d == 0) a.part_ml[p] = float2{top, sum};
-    }
-}
 
 // two codes of bytes `sel` picks, each under the fp16 exponent of 1024, minus `bias`
 __device__ __forceinline__ h2 byte_pair(uint32_t w, uint32_t sel, _Float16 bias)
@@ -373,6 +357,8 @@ struct BlockRegs {
 // p <= 2^kSlack, and the operand p * vscale * 2^(kTop - E) stays below 2^15.
 constexpr float kSlack = 8.f;
 constexpr int kTop = 6;
+// Exponents between a piece's sum of weights, as it is stored, and 1: results of any size have a sum over 2^12 pieces
+constexpr int kSumDown = 20;
 
 // Exponents of the value scales that some row of the item has seen: the largest and the smallest (0 has -127)
 struct ValueRange {
@@ -383,6 +369,26 @@ struct ValueRange {
         low = min(low, 128 - (int)(range >> 16));
     }
 };
+
+// 4 dims of a finished row: into y where its item is one piece, else among the pieces' results
+template <int D, bool BF16>
+__device__ __forceinline__ void put_result(const AttnArgs &a, const Span &t, int pieces, int slot, int kvh, int rows,
+                                           int rr, int d, f4 v, float top, float sum)
+{
+    if (pieces == 1) {
+        const int r = t.r0 + rr, i = a.by_group.of(r), h = a.by_group.rest(r);
+        const ushort4 w = {round_out<BF16>(v[0]), round_out<BF16>(v[1]), round_out<BF16>(v[2]), round_out<BF16>(v[3])};
+        *reinterpret_cast<ushort4 *>(a.y + ((int64_t)(t.s.row0 + i) * a.q_heads + kvh * a.group + h) * D + d) = w;
+    } else {
+        const int64_t p = ((int64_t)slot * a.kv.heads + kvh) * rows + rr;
+        *reinterpret_cast<f4 *>(a.part_o + p * D + d) = v;
+        if (d == 0) {
+            // sum * 2^top, the sum brought to [2^-kSumDown, 2^(1 - kSumDown))
+            const int e = sum > 0.f ? (int)(__float_as_uint(sum) >> 23) - 127 + kSumDown : 0;
+            a.part_ml[p] = float2{top + (float)e, ldexpf(sum, -e)};
+        }
+    }
+}
 
 // How a matrix instruction lays things out: COLS = 16 (16x16x32) or 32 (32x32x16) rows of the item are its columns; a lane
 // l has column l % COLS and, j being l / COLS, the tokens (64 / QN) * q + 4 j + e of a block, q < QN and e < 4, and as many

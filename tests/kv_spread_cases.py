@@ -72,3 +72,17 @@ def case(kind, fmt, D, dt, n, gap, long=False):
             for which in range(cache.arrays // 2):
                 cache.meta(1, which)[page, :, t] *= f[:, None]
     return cache, batch, q, float(np.float32(scale))
+
+
+def largest(fmt, D, n, long, offset):
+    """As above: bf16 values up to the type's largest (offset: all of one sign and close together), weights much alike."""
+    rng = np.random.default_rng(D + 7 * long)
+    lens = [3000, 2500] if long else [200, 150]
+    cache = filled(rng, fmt, 24 if long else 8, 256 if long else 64, 1, D, torch.bfloat16)
+    places = cache.pages * cache.page
+    x = rng.uniform(0.75, 1.0, (places, D)) if offset else rng.uniform(-1, 1, (places, D))
+    x = torch.from_numpy(np.ldexp(x, 127)).to(torch.bfloat16)
+    at = np.arange(places)
+    cache.put(1, at // cache.page, at % cache.page, 0, x.float().numpy())
+    batch = Batch(cache, n, lens, rng)
+    return cache, batch, rows(rng, batch.rows, 2, D, torch.bfloat16), float(np.float32(D ** -0.5 / 4))

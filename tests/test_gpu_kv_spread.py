@@ -4,7 +4,7 @@ import pytest
 
 import bit_weight_only_pack_amd as lb
 from kv_bounds import bounded
-from kv_spread_cases import case
+from kv_spread_cases import case, largest
 from kv_util import DT, assert_within, attend
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +41,14 @@ def test_spread_in_pieces(fmt, dt, kind, gap):
         batch.device()
         assert lb.lowbit_kv_attention_workspace_bytes(cache.handle(256), batch.handle(), 4) > 0
         check(cache, batch, q, scale, dt, str(n))
+
+
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("offset", [False, True])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("fmt", ["i8"])
+def test_values_up_to_the_largest(fmt, D, offset, long):
+    """Weighted means of finite values are finite, whatever many tokens' sums would be."""
+    for n in ([1, 2], [70, 130]):
+        cache, batch, q, scale = largest(fmt, D, n, long, offset)
+        check(cache, batch, q, scale, "bf16", str(n))
