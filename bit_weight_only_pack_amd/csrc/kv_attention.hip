@@ -357,6 +357,9 @@ struct BlockRegs {
 // p <= 2^kSlack, and the operand p * vscale * 2^(kTop - E) stays below 2^15.
 constexpr float kSlack = 8.f;
 constexpr int kTop = 6;
+// Exponents that minima are lowered by in their sums of p * minimum, so that minima up to the largest have one over 2^22
+// tokens, at p = 2^kSlack all of them; what is lost is 2^-119 a token.
+constexpr int kMinDown = 30;
 // Exponents between a piece's sum of weights, as it is stored, and 1: results of any size have a sum over 2^12 pieces
 constexpr int kSumDown = 20;
 
@@ -442,7 +445,7 @@ struct Rows {
     int see_lo[NQ], see_hi[NQ];          // tokens that the row sees
     Acc o[NQ][M];                        // sum p * vscale * 2^(kTop - E) * code, EL dims of the lane's column
     float mc[NQ], limit[NQ];             // exponent that the row's terms are taken to, and what they may pass it by
-    float l[NQ], bias[NQ];               // sums of the lane's p and p * vmin
+    float l[NQ], bias[NQ];               // sums of the lane's p, and of p * vmin * 2^-kMinDown
     int E;
     // Where the item's value scales spread by more than this, the row's own tokens may have small ones, or those that count
     // for much: its sums are then taken to the largest p * vscale so far, by 2^k more than to E.  Up to here the largest
@@ -579,7 +582,8 @@ struct Rows {
     __device__ __forceinline__ int unit(int x) const { return E - kTop - k[x]; }
 
     // acc: products of the queries with a block's codes; leaves the operand of the product with its values.  kl, vl (4
-    // bits): minima + 8 scales (the keys' with the factor of their scales); vs: times 2^(kTop - E).
+    // bits): minima + 8 scales (the keys' with the factor of their scales, the values' times 2^-kMinDown); vs: times
+    // 2^(kTop - E).
     // masked: some row does not see all of the block, whose first token is t0, or its page is missing.
     template <typename KS_, typename KL, typename VS, typename VL>
     __device__ __forceinline__ void weigh(Acc (&acc)[NQ][S::TILES], KS_ ks, KL kl, VS vs, VL vl, bool masked, bool paged,
@@ -814,7 +818,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     r.kl[q][e] = __builtin_fmaf(8.f, r.ks[q][e], r.kl[q][e]);
-                    r.vl[q][e] = __builtin_fmaf(8.f, r.vs[q][e], r.vl[q][e]);
+                    r.vl[q][e] = ldexpf(__builtin_fmaf(8.f, r.vs[q][e], r.vl[q][e]), -kMinDown);
                 }
         }
         const int64_t t0 = (int64_t)blk * kTile;
@@ -924,7 +928,7 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-            add += b_s[x][q][row] * (f[q] * inv);
+            add += ldexpf(b_s[x][q][row] * (f[q] * inv), kMinDown);
             g_s[x][q][row] = ldexpf(f[q] * inv, e_s[x][q][row]);
         }
         add_s[x][row] = add;
@@ -1120,7 +1124,7 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
             }
             if (wave == 1) {
                 at[A * 64] = ldexpf(scale[1], kTop - values.top);
-                if constexpr (!I8) at[3 * 64] = __builtin_fmaf(8.f, scale[1], low[1]);
+                if constexpr (!I8) at[3 * 64] = ldexpf(__builtin_fmaf(8.f, scale[1], low[1]), -kMinDown);
             }
         }
     };
@@ -1216,7 +1220,7 @@ __global__ __launch_bounds__(W * 64, W == 8 || D < 256 ? 2 : 1) void kv_attentio
 
     const float sum = Sh::sum_of(w.l[0]), low_sum = Sh::sum_of(w.bias[0]);
     if (n >= wn) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum, add = low_sum * inv;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum, add = ldexpf(low_sum * inv, kMinDown);
 #pragma unroll
     for (int i = 0; i < M; ++i)
 #pragma unroll

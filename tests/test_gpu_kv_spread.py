@@ -46,7 +46,7 @@ def test_spread_in_pieces(fmt, dt, kind, gap):
 @pytest.mark.parametrize("long", [False, True])
 @pytest.mark.parametrize("offset", [False, True])
 @pytest.mark.parametrize("D", [64, 256])
-@pytest.mark.parametrize("fmt", ["i8"])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
 def test_values_up_to_the_largest(fmt, D, offset, long):
     """Weighted means of finite values are finite, whatever many tokens' sums would be."""
     for n in ([1, 2], [70, 130]):
