@@ -485,7 +485,9 @@ struct Rows {
         const int j = lane / COLS, n = lane % COLS;
         us8 raw[NQ][KS];
         int top[NQ];                     // largest |q| of the row, its bits; 0 where there is none or no number
-        float all = a.scale2;
+        // infinite only where a scale of over 2^127 has become so; and as many exponents as it can be lowered by within binary32
+        float all = fminf(a.scale2, FLT_MAX);
+        const int most = (int)(__float_as_uint(all) >> 23) - 127 + 125;
         alike = true;
         E = ValueRange().top;
         spread = false;
@@ -498,7 +500,7 @@ struct Rows {
             see_lo[x] = a.window > 0 ? see_hi[x] - min(a.window, max(seq.len, 1)) : 0;
 #pragma unroll
             for (int k = 0; k < KS; ++k) raw[x][k] = *reinterpret_cast<const us8 *>(src + dims(k, j));
-            c[x] = EVEN ? 1.f : a.scale2;
+            c[x] = EVEN ? 1.f : all;
             qsum[x] = l[x] = bias[x] = mc[x] = 0.f;
             k[x] = 0;
             limit[x] = -INFINITY;
@@ -515,7 +517,8 @@ struct Rows {
         }
         if constexpr (BF16) {
             // into fp16 after a power of two that brings the largest value of the row, or of all rows if none's is smaller
-            // by more than 2^8, to [2^14, 2^15)
+            // by more than 2^8, to [2^14, 2^15), or as near to it as leaves the factor of its scores a normal number: 2^-25
+            // of fp16 are less than 2^-14 of a score then, whatever the keys
             int shift_all = 0;
             if constexpr (EVEN) {
                 int hi = 0, lo = 0x7fff;
@@ -526,12 +529,12 @@ struct Rows {
                 }
                 meet(hi, lo);
                 alike = lo >= hi || (hi >> 7) - (lo >> 7) <= 8;
-                shift_all = hi > 0 ? 141 - (hi >> 7) : 0;
+                shift_all = hi > 0 ? min(141 - (hi >> 7), most) : 0;
                 if (alike) all = ldexpf(all, -shift_all);
             }
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                const int own = top[x] > 0 ? 141 - (top[x] >> 7) : 0, shift = EVEN && alike ? shift_all : own;
+                const int own = top[x] > 0 ? min(141 - (top[x] >> 7), most) : 0, shift = EVEN && alike ? shift_all : own;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -547,7 +550,7 @@ struct Rows {
         }
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
-            if constexpr (!EVEN) c[x] = fminf(fmaxf(c[x], FLT_MIN), FLT_MAX);
+            c[x] = fminf(c[x], FLT_MAX);
             if constexpr (!I8) {
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
@@ -556,7 +559,7 @@ struct Rows {
                 qsum[x] = S::sum_of(qsum[x]);
             }
         }
-        return fminf(fmaxf(all, FLT_MIN), FLT_MAX);
+        return fminf(all, FLT_MAX);
     }
 
     // takes the sums to the exponents of the value scales as they are now: what they are to be multiplied by goes to `down`;

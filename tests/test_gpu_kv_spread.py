@@ -1,5 +1,6 @@
 """Attention over caches whose value scales are far apart, in both kernels and in pieces, within a bound that counts every
 token by its own weight and value scale: tokens that count for nothing, and those that other rows see, cost no bits."""
+import numpy as np
 import pytest
 
 import bit_weight_only_pack_amd as lb
@@ -52,3 +53,18 @@ def test_values_up_to_the_largest(fmt, D, offset, long):
     for n in ([1, 2], [70, 130]):
         cache, batch, q, scale = largest(fmt, D, n, long, offset)
         check(cache, batch, q, scale, "bf16", str(n))
+
+
+# queries, keys and scale times 2^these: scores of ordinary size
+@pytest.mark.parametrize("dt,q_by,k_by,by", [("bf16", -120, 118, 2), ("bf16", -126, 121, 5), ("bf16", -100, 0, 100),
+                                             ("bf16", 110, -105, -5), ("bf16", -60, 120, -60), ("bf16", -128, 120, 8),
+                                             ("f16", 3, 122, -125), ("f16", 0, 100, -100), ("f16", -3, -97, 100)])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_scores_of_small_and_large_factors(fmt, dt, q_by, k_by, by):
+    """Queries, keys and scales far from 1, whose product is not."""
+    for n in ([1, 2], [9, 15], [70, 40]):
+        cache, batch, q, scale = case("ladder", fmt, 64, dt, n, 0)
+        for which in range(cache.arrays // 2):
+            cache.meta(0, which)[:] = np.ldexp(cache.meta(0, which), k_by)
+        q = (q.double() * 2.0 ** q_by).to(q.dtype)
+        check(cache, batch, q, float(np.float32(np.ldexp(scale, by))), dt, str(n))
