@@ -548,6 +548,12 @@ struct Rows {
 #pragma unroll
                 for (int k = 0; k < KS; ++k) qf[x][k] = __builtin_bit_cast(h8, raw[x][k]);
         }
+        // a query that is not finite makes NaN of its row (q * 0 + q): scores of minus infinity are not told from hidden ones
+        const h8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) qf[x][k] = __builtin_elementwise_fma(qf[x][k], zero, qf[x][k]);
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             c[x] = fminf(c[x], FLT_MAX);

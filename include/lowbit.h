@@ -750,7 +750,7 @@ int lowbit_kv_read(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, v
  * row's largest.
  *   q         : [rows] rows of q_heads * dim values, LOWBIT_F16 or LOWBIT_BF16,
  *               16-byte aligned, q_stride values apart (at least q_heads * dim, a
- *               multiple of 8)
+ *               multiple of 8); a head of it that is not finite gives NaN
  *   q_heads   : a multiple of heads; head h reads the cache's head h / (q_heads / heads)
  *   scale     : finite and > 0
  *   window    : tokens that a row sees at most, its own included; 0: no limit

@@ -368,6 +368,28 @@ def test_nan_of_no_weight(fmt, D):
                 cache.b = b
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_queries_that_are_not_finite(fmt, dt):
+    """A row whose query holds an infinity or a NaN is NaN, of whatever sign its scores are; other rows are not touched."""
+    rng = np.random.default_rng(28)
+    D, dtype = 64, DT[dt][1]
+    for n, length in ((3, 100), (60, 200)):
+        cache = filled(rng, fmt, 4, 64, 1, D)
+        batch = Batch(cache, [n], [length], rng)
+        page, t = batch.where(cache, 0, np.arange(length))
+        cache.put(0, page, t, 0, rng.uniform(0.5, 1.5, (length, D)).astype(np.float32))     # keys above zero
+        batch.device()
+        data = cache.device()
+        for value in (float("-inf"), float("inf"), float("nan")):
+            q = rows(rng, n, 2, D, dtype).abs()
+            q[n // 2, 1, 5] = value
+            y = attend(cache.handle(data), batch, q.cuda(), 2 * D, 2, dt, 0.125, 0, n, D)
+            bad = torch.zeros((n, 2), dtype=torch.bool)
+            bad[n // 2, 1] = True
+            assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all(), (n, value)
+
+
 @pytest.mark.parametrize("heads,group", [(1, 1), (1, 64), (5, 3), (7, 1), (16, 2), (32, 1)])
 def test_head_layouts(heads, group):
     rng = np.random.default_rng(heads * 100 + group)
