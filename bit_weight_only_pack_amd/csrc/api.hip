@@ -864,8 +864,8 @@ bool kv_shape_ok(int fmt, int page_size, int heads, int dim)
            (dim == 64 || dim == 128 || dim == 256) && heads > 0 && heads <= kKvMaxHeads;
 }
 
-// Checks shared by the entry points of the key/value cache.  *empty: there is nothing to do.
-int check_kv(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool *empty)
+// What the sizes alone say.  *empty: there is nothing to do.
+int check_kv_sizes(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool *empty)
 {
     *empty = false;
     if (c == nullptr || b == nullptr) return LOWBIT_E_INVALID_ARG;
@@ -874,19 +874,7 @@ int check_kv(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool
     if (!kv_shape_ok(c->fmt, c->page_size, c->heads, c->dim)) return LOWBIT_E_UNSUPPORTED;
     if ((int64_t)b->table_width * c->page_size > ((int64_t)1 << 30) || b->count >= kGridLimit)
         return LOWBIT_E_UNSUPPORTED;
-    if (b->count == 0 || b->rows == 0 || b->max_rows == 0) {
-        *empty = true;
-        return LOWBIT_OK;
-    }
-    if (b->kv_len == nullptr || b->row_offsets == nullptr || (b->table_width > 0 && b->page_table == nullptr) ||
-        (c->pages > 0 && c->data == nullptr))
-        return LOWBIT_E_INVALID_ARG;
-    if (!aligned(c->data, 256) || !aligned(b->page_table, 4) || !aligned(b->kv_len, 4) || !aligned(b->row_offsets, 4))
-        return LOWBIT_E_INVALID_ARG;
-    a->data = static_cast<uint8_t *>(c->data);
-    a->table = b->page_table;
-    a->len = b->kv_len;
-    a->offsets = b->row_offsets;
+    *empty = b->count == 0 || b->rows == 0 || b->max_rows == 0;
     a->fmt = c->fmt;
     a->pages = c->pages;
     a->page_shift = c->page_size == 64 ? 6 : c->page_size == 128 ? 7 : 8;
@@ -897,6 +885,23 @@ int check_kv(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool
     a->count = b->count;
     a->rows = b->rows;
     a->max_rows = b->max_rows < b->rows ? b->max_rows : b->rows;
+    return LOWBIT_OK;
+}
+
+// Checks shared by the entry points of the key/value cache
+int check_kv(const lowbit_kv_cache *c, const lowbit_kv_batch *b, KvArgs *a, bool *empty)
+{
+    const int st = check_kv_sizes(c, b, a, empty);
+    if (st != LOWBIT_OK || *empty) return st;
+    if (b->kv_len == nullptr || b->row_offsets == nullptr || (b->table_width > 0 && b->page_table == nullptr) ||
+        (c->pages > 0 && c->data == nullptr))
+        return LOWBIT_E_INVALID_ARG;
+    if (!aligned(c->data, 256) || !aligned(b->page_table, 4) || !aligned(b->kv_len, 4) || !aligned(b->row_offsets, 4))
+        return LOWBIT_E_INVALID_ARG;
+    a->data = static_cast<uint8_t *>(c->data);
+    a->table = b->page_table;
+    a->len = b->kv_len;
+    a->offsets = b->row_offsets;
     return LOWBIT_OK;
 }
 
@@ -944,7 +949,7 @@ size_t lowbit_kv_attention_workspace_bytes(const lowbit_kv_cache *cache, const l
 {
     KvArgs a{};
     bool empty;
-    if (check_kv(cache, batch, &a, &empty) != LOWBIT_OK || empty) return 0;
+    if (check_kv_sizes(cache, batch, &a, &empty) != LOWBIT_OK || empty) return 0;
     if (q_heads <= 0 || q_heads % a.heads != 0 || q_heads > kKvMaxHeads || !kv_attention_fits(a, q_heads)) return 0;
     return kv_attention_workspace(a, q_heads);
 }

@@ -766,7 +766,8 @@ int lowbit_kv_attention(const lowbit_kv_cache *cache, const lowbit_kv_batch *bat
                         void *stream);
 
 /* Workspace bytes of lowbit_kv_attention (0 if none is needed or the sizes are
- * invalid).  It depends on the sizes alone: not on lengths, pages or offsets. */
+ * invalid).  It depends on the sizes alone: not on lengths, pages or offsets, whose
+ * pointers may be NULL yet. */
 size_t lowbit_kv_attention_workspace_bytes(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, int q_heads);
 
 #ifdef __cplusplus

@@ -101,3 +101,18 @@ def test_attention_workspace_is_checked():
         assert lb.lowbit_kv_attention_workspace_bytes(cache(), batch(), Hq) == 0
     for kw in (dict(count=0), dict(rows=0), dict(most=0), dict(count=-1), dict(width=1 << 25)):
         assert lb.lowbit_kv_attention_workspace_bytes(cache(), batch(**kw), 8) == 0
+
+
+def test_attention_workspace_is_known_before_the_buffers():
+    """The query takes the sizes alone: any pointer may be missing, or not be one yet."""
+    seen = 0
+    for count, most, width, dim in ((1, 1, 64, 128), (1, 5, 2048, 64), (4, 1, 512, 256), (2, 300, 512, 128), (3, 2, 1, 64)):
+        sizes = dict(count=count, rows=count * most, most=most, width=width)
+        nb = lb.lowbit_kv_attention_workspace_bytes(cache(dim=dim), batch(**sizes), 8)
+        seen += nb > 0
+        none = dict(table=None, lens=None, offs=None)
+        assert lb.lowbit_kv_attention_workspace_bytes(cache(data=None, dim=dim), batch(**sizes, **none), 8) == nb
+        assert lb.lowbit_kv_attention_workspace_bytes(cache(data=FAKE + 8, dim=dim), batch(**sizes), 8) == nb
+        for name in none:
+            assert lb.lowbit_kv_attention_workspace_bytes(cache(dim=dim), batch(**sizes, **{name: None}), 8) == nb
+    assert seen >= 3
