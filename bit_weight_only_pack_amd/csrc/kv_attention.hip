@@ -117,8 +117,9 @@ __device__ __forceinline__ Span attn_span(const AttnArgs &a, int b, int tile, in
 // blocks makes ceil(n / size) pieces, so `there` items of T blocks in all make about T / size + there / 2.  Few rows, bound
 // by memory: T / size as many as are resident at once, or twice that where many items leave odd ends.  Tiles, bound by the
 // compute units: pieces to fill these once, or a whole number of times, and those of an item are then made alike (a chunk of
-// 1024 tokens over 4096, 4 heads of 256: 70 us for 72; few rows beside it: 44 for 36, as odd ends fill what is left).
-// Nothing is cut where no item is much longer than a piece.  Those of items that are cut, at most 2 T / size, have slots for
+// 1024 tokens over 4096, 4 heads of 256: 70 us for 72; few rows beside it: 44 for 36, as odd ends fill what is left), once
+// more where the odd ends alone nearly do (8 heads of 64, 50 rows over 131072 tokens beside 125 times 50 over 1024: 195 us,
+// 2918 with a piece of everything).  Nothing is cut where no item is much longer than a piece.  Those of items that are cut, at most 2 T / size, have slots for
 // their results.  Every wave works this out for itself from the lengths, 64 items at a time, the last tiles of a sequence,
 // its longest, first.
 struct Piece {
@@ -163,7 +164,11 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, int rows, int want
     }
     total = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)total, plus), 63);
     most = __builtin_amdgcn_readlane(wave_scan(most, larger), 63);
-    const int wanted = a.fill ? (there / 2 / a.share + 1) * a.share - there / 2 : there > a.share / 2 ? 2 * a.share : a.share;
+    int wanted = there > a.share / 2 ? 2 * a.share : a.share;
+    if (a.fill) {
+        wanted = (there / 2 / a.share + 1) * a.share - there / 2;
+        if (wanted * 2 < a.share) wanted += a.share;     // so few would make a piece of everything
+    }
     const int64_t share = (((int64_t)total << 2) + wanted - 1) / wanted;
     const int even = (int)min(max(share, (int64_t)kMinPiece), (int64_t)1 << 25);     // past any item's blocks
     o.size = __builtin_amdgcn_readfirstlane(most <= even + even / 2 ? max(most, 1) : even);

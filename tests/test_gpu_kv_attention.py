@@ -443,6 +443,30 @@ def test_offsets_that_go_back():
     assert (ws[need:] == 0x5A).all() and (y[rows_:] == 7).all()
 
 
+@pytest.mark.parametrize("B", [13, 14, 16, 31])
+def test_one_long_sequence_among_tiles(B):
+    """A tile over many tokens is cut, whatever the number of short ones beside it."""
+    rng = np.random.default_rng(29)
+    heads, D, n, dtype = 32, 256, 20, torch.bfloat16                  # 8 workgroups a head are resident
+    cache = filled(rng, "i8", 3, 256, heads, D)
+    batch = Batch(cache, [n] * B, [0] * B, rng, width=16)
+    batch.lens = [4096] + [130] * (B - 1)
+    batch.table = rng.integers(0, cache.pages, (B, 16)).astype(np.int32)
+    handle, ch = batch.device(), cache.handle(cache.device())
+    q = rows(rng, batch.rows, heads, D, dtype)
+    need = lb.lowbit_kv_attention_workspace_bytes(ch, handle, heads)
+    ws = torch.full((need,), 0x5A, dtype=torch.uint8, device="cuda")
+    y = torch.zeros((batch.rows, heads, D), dtype=dtype, device="cuda")
+    lb.check(lb.lowbit_kv_attention(ch, handle, q.cuda(), heads * D, heads, lb.LOWBIT_BF16, 0.1, 0, y, ws, need))
+    torch.cuda.synchronize()
+    # results of at least two pieces of 20 rows of every head
+    assert (ws != 0x5A).sum().item() > 2 * heads * n * D * 4 * 0.9
+    first = Batch(cache, [n] * 2, [0] * 2, rng, width=16)            # the long one and one of the others
+    first.lens, first.table = batch.lens[:2], batch.table[:2]
+    want, bound = attention64(cache, first, q[:2 * n].double().numpy(), float(np.float32(0.1)), 0, dtype)
+    assert_within(y[:2 * n], want, bound)
+
+
 def test_graphs_that_share_a_workspace():
     """A chunk's graph and a decode step's, captured without a call before them, replayed in turn on one workspace."""
     rng = np.random.default_rng(25)
