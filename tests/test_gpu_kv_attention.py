@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import bit_weight_only_pack_amd as lb
+from kv_bounds import bounded
 from kv_util import DT, Batch, Cache, assert_within, attend, attention64, rows
 
 pytestmark = pytest.mark.gpu
@@ -64,6 +65,26 @@ def test_attention(fmt, D, dt):
         cache = filled(rng, fmt, 14 if page == 64 else 8, page, heads, D, DT[dt][1])
         batch = Batch(cache, n, lens, rng, extra_rows=case % 3)
         check(cache, batch, group, dt, rng, strided=case % 2 == 1, what="case %d" % case)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["i8", "u4"])
+def test_attention_token_by_token(fmt, D, dt):
+    """The same within bounds that count each token by its own weight: one part of p for two is told by them."""
+    for case, (group, n, lens) in enumerate(SHAPES + [(2, [60, 20], [500, 100])]):
+        rng = np.random.default_rng(200 * D + case)
+        page, heads = (64, 128, 256)[case % 3], 1 + case % 2
+        cache = filled(rng, fmt, 14 if page == 64 else 8, page, heads, D, DT[dt][1])
+        batch = Batch(cache, n, lens, rng)
+        batch.device()
+        window = (0, 0, 90)[case % 3]
+        q = rows(rng, batch.rows, heads * group, D, DT[dt][1])
+        for scale in (0.04, 0.004):
+            y = attend(cache.handle(cache.device()), batch, q.cuda(), heads * group * D, heads * group, dt, scale, window,
+                       batch.rows, D)
+            want, bound = bounded(cache, batch, q.double().numpy(), float(np.float32(scale)), window, DT[dt][1])
+            assert_within(y, want, bound, "case %d" % case)
 
 
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 200, 2 ** 31 - 1])
