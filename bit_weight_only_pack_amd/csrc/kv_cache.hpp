@@ -62,7 +62,7 @@ __device__ __forceinline__ uint8_t *kv_part(const KvArgs &a, int page, int head)
 constexpr int kv_blocks(int rows) { return (int)(((int64_t)rows + 62) / 64 + 1); }
 inline bool kv_rows_fit(const KvArgs &a)
 {
-    return (int64_t)a.count * (a.max_rows == 1 ? 1 : kv_blocks(a.max_rows)) * 2 * a.heads < ((int64_t)1 << 24);
+    return (int64_t)a.count * kv_blocks(a.max_rows) * 2 * a.heads < ((int64_t)1 << 24);
 }
 
 hipError_t launch_kv_write(const KvArgs &a, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int bf16,

@@ -710,6 +710,12 @@ typedef struct lowbit_kv_batch {
     int max_rows;                /* at least the most rows that one sequence has: sizes the grid
                                     (rows of a sequence past it are left out)                    */
 } lowbit_kv_batch;
+/*
+ * One launch has to hold a call, else LOWBIT_E_UNSUPPORTED: writing and reading,
+ * count * ((max_rows + 62) / 64 + 1) * heads < 2^23; attention, some 2^31 for
+ * count * max_rows * q_heads, a sequence's rows rounded up to a tile of 128 rows *
+ * group.  A max_rows near the real one keeps calls of many sequences far below.
+ */
 
 /* Bytes of one page (0 for an invalid combination; a multiple of 256 * heads). */
 size_t lowbit_kv_page_bytes(int fmt, int page_size, int heads, int dim);
