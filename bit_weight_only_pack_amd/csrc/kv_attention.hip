@@ -1381,10 +1381,11 @@ void cut_plan(AttnPlan &p, const KvArgs &a, int group, int64_t most_rows, int pl
     p.share = cut ? std::max(places / a.heads, 1) : 0;
     // tiles that there can be: whole ones of all rows, and a sequence's last
     const int64_t there = std::min(items, (int64_t)a.rows * group / p.rows + std::min(a.count, a.rows));
-    // T / size is at most 2 * share; a cut item has two pieces or more
-    const int64_t most = 2 * p.share;
-    p.pieces = cut ? there + most : items;
-    p.slots = 2 * most;
+    // T / size is at most 2 * share, 1.5 * share for tiles, and a cut item's pieces less than twice its part of that; nor are
+    // they more than its table's blocks make of kMinPiece each
+    const int64_t most = 2 * (int64_t)p.share, least = (blocks + kMinPiece - 1) / kMinPiece;
+    p.pieces = cut ? std::min(there + most, items * least) : items;
+    p.slots = std::min(p.tile ? 3 * (int64_t)p.share : 2 * most, items * least);
     p.cuts = (int)std::min<int64_t>(there, most);
 }
 // one launch or two: sequences of many rows first

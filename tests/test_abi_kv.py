@@ -116,3 +116,16 @@ def test_attention_workspace_is_known_before_the_buffers():
         for name in none:
             assert lb.lowbit_kv_attention_workspace_bytes(cache(dim=dim), batch(**sizes, **{name: None}), 8) == nb
     assert seen >= 3
+
+
+def test_attention_workspace_is_for_pieces_that_there_can_be():
+    """A piece is 4 blocks of 64 tokens or more: a short table makes few of them, whatever the compute units could take."""
+    for dim, rows, group in ((128, 40, 1), (64, 70, 2), (256, 20, 1), (64, 3, 4), (128, 5, 2)):
+        for heads in (1, 8, 512):
+            for count in (1, 3):
+                for blocks in (17, 18, 40, 1000, 5000):
+                    b = batch(count=count, rows=rows * count, most=rows, width=blocks)
+                    nb = lb.lowbit_kv_attention_workspace_bytes(cache(dim=dim, heads=heads), b, heads * group)
+                    items = count * -(-rows * group // 16)               # of the narrowest kind
+                    one = heads * (128 if rows * group > 64 else 64) * (dim * 4 + 8)
+                    assert 0 < nb <= 2 * (items * -(-blocks // 4) * one + 1025 * 16), (dim, heads, count, blocks, nb)

@@ -488,6 +488,28 @@ def test_one_long_sequence_among_tiles(B):
     assert_within(y[:2 * n], want, bound)
 
 
+@pytest.mark.parametrize("n", [[1], [40], [130], [1, 3, 70], [130, 20, 40]])
+@pytest.mark.parametrize("D", [64, 256])
+def test_nothing_behind_the_workspace_is_written(D, n):
+    """Workspaces of tables that are short enough to limit the pieces, filled as far as they are asked for."""
+    rng = np.random.default_rng(30)
+    cache = filled(rng, "i8", 12, 64, 2, D)
+    for blocks in (17, 20, 24, 33, 70):
+        batch = Batch(cache, n, [0] * len(n), rng, width=blocks)
+        batch.lens = [64 * blocks - 7 * b for b in range(len(n))]
+        batch.table = rng.integers(0, cache.pages, (len(n), blocks)).astype(np.int32)
+        handle, ch, q = batch.device(), cache.handle(cache.device()), rows(rng, batch.rows, 4, D, torch.float16)
+        need = lb.lowbit_kv_attention_workspace_bytes(ch, handle, 4)
+        assert need > 0
+        ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+        y = torch.zeros((batch.rows, 4, D), dtype=torch.float16, device="cuda")
+        lb.check(lb.lowbit_kv_attention(ch, handle, q.cuda(), 4 * D, 4, lb.LOWBIT_F16, 0.06, 0, y, ws, need))
+        torch.cuda.synchronize()
+        assert (ws[need:] == 0x5A).all(), blocks
+        want, bound = attention64(cache, batch, q.double().numpy(), float(np.float32(0.06)), 0, torch.float16)
+        assert_within(y, want, bound, "%d blocks" % blocks)
+
+
 def test_graphs_that_share_a_workspace():
     """A chunk's graph and a decode step's, captured without a call before them, replayed in turn on one workspace."""
     rng = np.random.default_rng(25)
