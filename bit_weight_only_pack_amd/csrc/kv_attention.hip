@@ -25,10 +25,10 @@
 //
 // Two kernels share this.  Few rows (kv_attention_kernel) read the cache once,
 // and its bytes are the bound: 562 MB of 8 bit cache for one token each of 64
-// sequences of up to 8192 in 107 us, 5.2 TB/s, as fast as a large copy.  Many rows
+// sequences of up to 8192 in 108 us, 5.2 TB/s, as fast as a large copy.  Many rows
 // (kv_attention_tile_kernel) are bound by the instructions of a compute unit,
-// matrix and vector ones: 515 GFLOP of a causal prompt in 0.57 ms, 900 TFLOP/s,
-// 74 % of a large library product's rate.
+// matrix and vector ones: 515 GFLOP of a causal prompt in 0.59 to 0.61 ms, 850 to
+// 870 TFLOP/s, 70 % of a large library product's rate.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -43,7 +43,10 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTile = 64;                // tokens of a step: one block of a page
-constexpr int kMaxItems = 512;           // items that are cut into pieces
+// Items up to which they are cut, counted as sequences times the tiles of the longest, for so many fit a wave's registers (8 a
+// lane).  Past it a long item is walked whole: 1024 rows of 4 heads of 256, group 2, over 4096 tokens, 112 us beside 31 single
+// rows and 206 beside 32; single rows of 512 sequences, one of 65536 tokens, 171 us, of 513 438.
+constexpr int kMaxItems = 512;
 constexpr int kMinPiece = 4;             // blocks that a workgroup takes at least: one for each wave
 
 // n / d and n % d for 0 <= n < 2^31 by one product: m = ceil(2^(31 + b) / d) with 2^(b - 1) < d <= 2^b
@@ -454,7 +457,9 @@ struct Rows {
     int E;
     // Where the item's value scales spread by more than this, the row's own tokens may have small ones, or those that count
     // for much: its sums are then taken to the largest p * vscale so far, by 2^k more than to E.  Up to here the largest
-    // operand is at least 2^(kTop - SPREAD), 2^23 (bf16 results: 2^17) times what fp16 rounds next to zero.
+    // operand is at least 2^(kTop - SPREAD), 2^23 (bf16 results: 2^17) times what fp16 rounds next to zero.  A row's own
+    // exponents take a maximum and two steps more for each operand: a prompt 656 us for 595, a window 170 for 161, decode 116.4
+    // for 116.1, so they are not taken where scales are alike.
     static constexpr int SPREAD = BF16 ? 14 : 8;
     static constexpr int NONE = 1 << 20; // k of a row that has no sums yet
     bool spread;
@@ -755,9 +760,9 @@ struct Rows {
 // block's loads are under way while the one before is worked on: its keys are asked for as soon as the last product with the
 // keys before them has begun, scales and values likewise, so that they need no registers of their own.
 //
-// Bound by bytes where many workgroups are resident (decode, 8 bits, 562 MB: 107 us), by a wave's own instructions where few
+// Bound by bytes where many workgroups are resident (decode, 8 bits, 562 MB: 108 us), by a wave's own instructions where few
 // are: a block is some 800 of them, 4000 clocks, whatever the number of waves beside it (one sequence of 777 tokens, 8
-// heads: 11.0 us with 4 waves, 11.7 with 8; of 500 tokens 8.3 and 9.3).
+// heads: 11.4 us; before value scales had their range taken, 11.0 with 4 waves, 11.7 with 8; of 500 tokens 8.3 and 9.3).
 template <int FMT, int D, bool BF16, int NQ>
 __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel(AttnArgs a)
 {
@@ -977,7 +982,8 @@ __global__ __launch_bounds__(256, D * NQ > 128 ? 1 : 2) void kv_attention_kernel
 
 // Many rows: a workgroup has kTileRows rows of an item, COLS in each of its W waves, and takes the blocks of its piece one by
 // one.  Codes become fp16 operands once for all waves and lie in LDS in the order in which a wave reads them, 16 bytes a lane:
-// no bank conflicts, and no permutation.
+// no permutation, and no bank conflicts.  The 8-byte stores of values for 32x32x16 meet half of the banks twice: 15.8e6 cycles in
+// a prompt of 15.8e6 products.
 //
 // A block is two phases of a wave: M, the products (of the values of the block before, and of the block's keys) with the
 // unpacking of what comes next between them, and S, the softmax.  One barrier a block stands between the two: what M(i)
@@ -1352,8 +1358,9 @@ constexpr int kWholeBlocks = 16;
 // heads of 256, take 118 us so, 178 all in tiles.
 constexpr int64_t kFewBeside = 16;
 // Rows of a sequence that the kernel for few takes: as many as its registers hold.  A tile does the products of 128 rows
-// whatever there are.  8 bits, sequences of up to 4001 tokens: 24 of 40 rows, 2 heads of 64, 22.2 us, 28.4 in tiles; 16 of 32
-// rows, 4 heads of 128, 23.6 and 36.4; 16 of 16 rows, 4 heads of 256, 26.1 and 39.8.
+// whatever there are.  8 bits, sequences of up to 4001 tokens: 24 of 40 rows, 2 heads of 64, 21.6 us, 29.2 in tiles (of 64 rows
+// 23.8 and 29.9; 4 bits 24.8 and 32.9, of 64 rows 26.9 and 34.0); 16 of 32 rows, 4 heads of 128, 23.6 and 36.4; 16 of 16 rows,
+// 4 heads of 256, 26.1 and 39.8.
 int64_t few_rows(int dim) { return dim == 64 ? 64 : dim == 128 ? 32 : 16; }
 // Workgroups that are resident at once, which the pieces fill: two on a compute unit, one where LDS (tiles of 256 dims) or
 // registers (few rows, more than 128 sums a lane) leave room for no more.  Few rows, with the other of 256 and 512: 562 MB
