@@ -16,12 +16,13 @@
 // tokens (values): s = kscale * acc (+ kmin * sum of q, 4 bits), and the fp16
 // operand is p * vscale * 2^(kTop - E), E the largest exponent of a value scale
 // so far; where scales differ by more than 2^8 (bf16 results: 2^14), each row
-// takes its operands to the largest of its own instead (Rows::SPREAD).  The minima of values enter as sum p * vmin, one number per row.  The
-// softmax runs in one pass; the maximum that a row's terms are taken to moves
-// only where one passes it by 2^kSlack, so that most blocks rescale nothing.
-// The operand stays under 2^(kSlack + kTop + 1) = 2^15, and terms down to 2^-20 of
-// one at that maximum and scale keep all their 11 bits (fp16's least normal
-// number is 2^-14).
+// takes its operands to the largest of its own instead (Rows::SPREAD).  The
+// minima of values enter as sum p * vmin, one number per row.  The softmax runs
+// in one pass; the maximum that a row's terms are taken to, a whole exponent,
+// moves only where one passes it by 2^kSlack, so that most blocks rescale
+// nothing.  The operand stays under 2^(kSlack + kTop + 1) = 2^15, and terms down
+// to 2^-20 of one at that maximum and scale keep all their 11 bits (fp16's least
+// normal number is 2^-14).
 //
 // Two kernels share this.  Few rows (kv_attention_kernel) read the cache once,
 // and its bytes are the bound: 562 MB of 8 bit cache for one token each of 64

@@ -712,9 +712,10 @@ typedef struct lowbit_kv_batch {
 } lowbit_kv_batch;
 /*
  * One launch has to hold a call, else LOWBIT_E_UNSUPPORTED: writing and reading,
- * count * ((max_rows + 62) / 64 + 1) * heads < 2^23; attention, some 2^31 for
- * count * max_rows * q_heads, a sequence's rows rounded up to a tile of 128 rows *
- * group.  A max_rows near the real one keeps calls of many sequences far below.
+ * count * ((max_rows + 62) / 64 + 1) * heads < 2^23; attention, count * heads *
+ * (tiles of 128 in max_rows * q_heads / heads) < 2^22, some thousands less where
+ * heads are thousands.  A max_rows near the real one keeps calls of many sequences
+ * far below.
  */
 
 /* Bytes of one page (0 for an invalid combination; a multiple of 256 * heads). */
@@ -753,7 +754,7 @@ int lowbit_kv_read(const lowbit_kv_cache *cache, const lowbit_kv_batch *batch, v
  * bits) after a power of two: it is off by half a step, or by 2^-23 (bf16 results:
  * 2^-17) of the row's largest such product.  So does q if it is bf16: what is below
  * 2^-31 of its row's largest counts for nothing, as do weights below 2^-100 of the
- * row's largest.
+ * row's largest; values below 2^-100 (bf16) may lose bits.
  *   q         : [rows] rows of q_heads * dim values, LOWBIT_F16 or LOWBIT_BF16,
  *               16-byte aligned, q_stride values apart (at least q_heads * dim, a
  *               multiple of 8); a head of it that is not finite gives NaN
